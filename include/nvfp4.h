@@ -346,6 +346,92 @@ nvfp4_status nvfp4_kv_scale_from_amax(const float* amax, float* scale, void* str
 nvfp4_status nvfp4_kv_quantize_e4m3(const void* x, int64_t rows, int64_t cols, int64_t ld,
                                     const float* scale, uint8_t* out, int64_t ldo, void* stream);
 
+/* 8-bit-integer (W8A8) linear layer: int8 codes in [-127, 127] with one FP32
+ * scale per row, for activations (a row is a token) and weights (a row is an
+ * output channel), beside the 4-bit layer for the projections that keep eight
+ * bits.  A [rows, cols] tensor of codes is contiguous.
+ *
+ * nvfp4_int8_quantize: codes and scales of x[rows, cols] (BF16, row stride ld,
+ * device).  Per row, every step one binary32 operation:
+ *   T = max(max |x|, 2^-100),  codes = RNE(fl32(x * fl32(127 / T))),
+ *   scale = fl32(T / 127).
+ * An all-zero row has scale 1.  A row that holds a NaN or an infinity gets
+ * scale NaN and codes 0: its products are NaN, other rows are not touched.
+ *   codes (device, rows * cols bytes), scale (device, rows FP32).
+ * Requirements: cols % 16 == 0, cols >= 16, ld % 8 == 0, ld >= cols; x and
+ * codes 16-byte aligned, scale 4-byte.  rows == 0 enqueues nothing.
+ * Errors: NVFP4_ERR_INVALID_ARG (null pointer, negative size, ld < cols, codes
+ * or scale overlapping x or one another), NVFP4_ERR_ALIGNMENT (cols, ld or a
+ * pointer), NVFP4_ERR_UNSUPPORTED_SHAPE (cols == 0, the size bounds),
+ * NVFP4_ERR_DEVICE, CUDA errors.  Asynchronous on `stream`.
+ * Source: the pages quantize every linear layer's weights and activations at
+ * run time (chatpaper.ai abstract) in 4 bits; the 8-bit form is the textbook
+ * symmetric one, which the pages do not give. */
+nvfp4_status nvfp4_int8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld,
+                                 int8_t* codes, float* scale, void* stream);
+
+/* Residual addition, root-mean-square norm and int8 quantization of its rows,
+ * the step in front of a layer's first projection, in one pass:
+ *   r = fl32(x + residual)  (r = x without a residual),
+ *   v = r * fl32(weight + weight_offset) / sqrt(mean(r^2) + eps),
+ * codes and scale those of v: with t = fl32(r * fl32(weight + weight_offset)),
+ * T = max(max |t|, 2^-100) over the row,
+ *   codes = RNE(fl32(t * fl32(127 / T))),
+ *   scale = fl32(fl32(T / 127) * rstd),  rstd = 1 / sqrt(mean(r^2) + eps)
+ * (the factor rstd is common to the row, so the codes do not depend on it).
+ * residual_out receives r rounded once to BF16; the norm reads r unrounded.
+ * A row whose t is zero throughout has scale 1.  A row with a NaN or an
+ * infinity in x, residual, r or t, or whose sum of squares exceeds binary32,
+ * gets scale NaN and codes 0 (residual_out holds r all the same).
+ *   x, residual, residual_out (device) BF16 [rows, cols], row strides ldx, ldr,
+ *     ldo elements; residual may be NULL (ldr unused); residual_out may be
+ *     NULL (ldo unused) and must be NULL without a residual.  residual_out may
+ *     be x or residual itself (same address and stride): the sum is then
+ *     written in place.  Any other overlap of an output with an input or
+ *     another output is refused.
+ *   weight (device) BF16 [cols]; weight_offset 0, or 1 for weights stored as
+ *     their difference from one (any finite value below 2^127 is accepted).
+ *   eps in [2^-126, 2^127).
+ *   codes (device, rows * cols bytes), scale (device, rows FP32).
+ * Requirements: cols % 16 == 0, cols >= 16, strides % 8 == 0 and >= cols;
+ * matrices, weight and codes 16-byte aligned, scale 4-byte.  rows == 0
+ * enqueues nothing.
+ * Errors: NVFP4_ERR_INVALID_ARG (null pointer, negative size, a stride below
+ * cols, eps or weight_offset out of range, residual_out without residual, an
+ * overlap), NVFP4_ERR_ALIGNMENT, NVFP4_ERR_UNSUPPORTED_SHAPE (cols == 0, the
+ * size bounds), NVFP4_ERR_DEVICE, CUDA errors.  Asynchronous on `stream`.
+ * Source: the hybrid model's blocks (evolve.pub review, Scope & Claims) put a
+ * norm in front of every quantized projection; the formula is the textbook
+ * root-mean-square norm -- the pages give none. */
+nvfp4_status nvfp4_add_rms_norm_int8(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                                     const void* weight, float weight_offset, float eps,
+                                     int64_t rows, int64_t cols, void* residual_out, int64_t ldo,
+                                     int8_t* codes, float* scale, void* stream);
+
+/* W8A8 GEMM with a scale per token and per channel:
+ *   acc[m, n] = sum_k a[m, k] * w[n, k]  (exact, 32-bit integers),
+ *   y[m, n] = BF16_RNE(fl32(fl32(fl32(acc) * a_scale[m]) * w_scale[n])).
+ * Integer sums are exact in any order, so a result depends on its own row of
+ * A and W alone, bit for bit: not on M, N or how the work is split.  Several
+ * modules fuse by concatenating their codes and scales along N.
+ *   a_codes [M, K], w_codes [N, K] int8 (device, contiguous, any codes
+ *     -128..127); a_scale [M], w_scale [N] FP32 (device).
+ *   y [M, N] BF16 (device), row stride ldy elements.
+ * Requirements: K % 16 == 0, 16 <= K <= 131056 (no sum can overflow);
+ * ldy >= N, ldy % 8 == 0; codes and y 16-byte aligned, scales 4-byte; y
+ * overlaps no input.  M == 0 or N == 0 enqueues nothing.
+ * Errors: NVFP4_ERR_INVALID_ARG (null pointer, negative size, an input inside
+ * y), NVFP4_ERR_ALIGNMENT (ldy or a pointer), NVFP4_ERR_UNSUPPORTED_SHAPE (K,
+ * the size bounds), NVFP4_ERR_DEVICE (not sm_100), CUDA errors; a bounded wait
+ * that gives up inside the kernel is reported later by
+ * nvfp4_last_device_status.  Asynchronous on `stream`.
+ * Source: every linear layer runs on quantized weights and activations
+ * (chatpaper.ai abstract); this is the layer in 8-bit integers, which the
+ * pages do not give. */
+nvfp4_status nvfp4_int8_gemm(const int8_t* a_codes, const float* a_scale, const int8_t* w_codes,
+                             const float* w_scale, void* y, int64_t ldy, int64_t M, int64_t N,
+                             int64_t K, void* stream);
+
 /* The whole W4A4 linear layer from host buffers, on one stream: the BF16
  * activation x_host [M, K] is copied into x_dev, its global scale (a_g,
  * a_amax) and NVFP4 codes (a_codes, a_sf in the tensor-core layout)

@@ -30,6 +30,7 @@ __all__ = [
     "ACT_NONE", "ACT_DECAY_GATE", "ACT_SIGMOID",
     "global_scale", "sf_bytes", "quantize", "quantize_into", "quantize_tensor",
     "gemm", "fused_gemm", "FusedWeight", "linear", "silu_mul", "mlp", "interleave_gate_up", "gemm_silu_mul", "harmonize", "kv_scale", "kv_quantize", "last_device_status",
+    "Int8Tensor", "int8_quantize", "int8_quantize_tensor", "add_rms_norm_int8", "int8_gemm",
     "save_quantized", "load_quantized", "linear_host", "HostLinearScratch",
     "debug_wait_timeout", "library_path",
 ]
@@ -380,10 +381,16 @@ def fused_gemm(a: QuantizedTensor, w_codes: torch.Tensor, w_sf: torch.Tensor,
     return y
 
 
-def linear(x: torch.Tensor, w, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """W4A4 linear layer: quantize the BF16 activation x at run time, then the
-    (fused) NVFP4 GEMM against a pre-quantized weight (QuantizedTensor or
-    FusedWeight)."""
+def linear(x, w, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Quantized linear layer: quantize the BF16 activation x at run time, then
+    the GEMM against a pre-quantized weight.  W4A4 for a QuantizedTensor or
+    FusedWeight; W8A8 for an Int8Tensor, whose x may also be an Int8Tensor that
+    add_rms_norm_int8 (or int8_quantize_tensor) made."""
+    if isinstance(w, Int8Tensor):
+        a = x if isinstance(x, Int8Tensor) else int8_quantize_tensor(x, stream=stream)
+        return int8_gemm(a, w, y, stream)
+    if isinstance(x, Int8Tensor):
+        raise TypeError("an Int8Tensor activation needs an Int8Tensor weight")
     a = quantize_tensor(x, stream=stream)
     if isinstance(w, FusedWeight):
         return fused_gemm(a, w.codes, w.sf, w.segments(), y, stream)
@@ -521,6 +528,8 @@ def gemm_silu_mul(a: QuantizedTensor, w_interleaved: QuantizedTensor,
 
 def mlp(x: torch.Tensor, w_gate_up, w_down, stream=None, interleaved: bool = False) -> torch.Tensor:
     """W4A4 SiLU-gated MLP: gate_up GEMM, SiLU(gate)*up, requantization, down GEMM.
+    Either weight may be an Int8Tensor instead: that projection then runs in
+    8-bit integers (and x may be an Int8Tensor for an Int8Tensor w_gate_up).
 
     With ``interleaved=True`` the gate_up weight is a QuantizedTensor whose
     rows interleave_gate_up arranged: SiLU(gate)*up and the global scale of h
@@ -564,6 +573,159 @@ def kv_quantize(x: torch.Tensor, scale: torch.Tensor, out: Optional[torch.Tensor
 
 
 # ---------------------------------------------------------------------------
+# 8-bit integers (W8A8): int8 codes with one FP32 scale per row, for the
+# projections that keep eight bits
+# ---------------------------------------------------------------------------
+@dataclass
+class Int8Tensor:
+    """Codes [rows, cols] int8 (contiguous) and one FP32 scale per row [rows]
+    in device memory: row r stands for codes[r] * scale[r]."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def cols(self) -> int:
+        return self.codes.shape[1]
+
+    @classmethod
+    def cat(cls, tensors: Sequence["Int8Tensor"]) -> "Int8Tensor":
+        """Several modules' weights concatenated along N for one GEMM: every
+        channel has its own scale, so the fused result equals the modules' own
+        bit for bit."""
+        return cls(torch.cat([t.codes for t in tensors]), torch.cat([t.scale for t in tensors]))
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride in elements; a single row has none of its own."""
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+
+
+def _empty(shape, dtype, device, stream):
+    """torch.empty for a kernel on `stream`: with an explicit stream the memory
+    is that stream's, so that no earlier use of it on another one can still be
+    running, and it is kept from reuse until the current stream is done with
+    it as well."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _check_codes(t, name: str, shape=None):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int8 or t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 2-D int8 tensor")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _check_row_scale(t, name: str, rows: int):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_contiguous() \
+            or t.numel() != rows:
+        raise ValueError(f"{name} must be a contiguous float32 tensor of {rows} elements")
+
+
+def int8_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
+                  scale: Optional[torch.Tensor] = None, stream=None):
+    """int8 codes [rows, cols] and FP32 scales [rows] of a BF16 matrix:
+    codes = RNE(x * (127 / max|row|)), scale = max|row| / 127."""
+    _check_bf16_matrix(x, "x")
+    rows, cols = x.shape
+    if codes is not None:
+        _check_codes(codes, "codes", x.shape)
+    if scale is not None:
+        _check_row_scale(scale, "scale", rows)
+    dev = _check_devices(x=x, codes=codes, scale=scale)
+    if codes is None:
+        codes = _empty((rows, cols), torch.int8, dev, stream)
+    if scale is None:
+        scale = _empty((rows,), torch.float32, dev, stream)
+    _lib.check("nvfp4_int8_quantize", _lib.lib().nvfp4_int8_quantize(
+        x.data_ptr(), rows, cols, _ld(x), codes.data_ptr(), scale.data_ptr(), _stream(stream)))
+    return codes, scale
+
+
+def int8_quantize_tensor(x: torch.Tensor, stream=None) -> Int8Tensor:
+    """int8_quantize as an Int8Tensor: an activation with a scale per token, or
+    a weight [N, K] with a scale per output channel."""
+    return Int8Tensor(*int8_quantize(x, stream=stream))
+
+
+def add_rms_norm_int8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                      eps: float = 1e-6, weight_offset: float = 0.0,
+                      residual_out: Optional[torch.Tensor] = None,
+                      codes: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                      stream=None):
+    """Residual addition, root-mean-square norm and int8 quantization in one
+    pass: r = x + residual, v = r * (weight + weight_offset) / sqrt(mean(r^2) + eps),
+    quantized per row.  Returns (Int8Tensor of v, r in BF16); the second is
+    None without a residual.  residual_out may be residual or x (in place)."""
+    _check_bf16_matrix(x, "x")
+    rows, cols = x.shape
+    if not isinstance(weight, torch.Tensor) or weight.dtype != torch.bfloat16 \
+            or weight.shape != (cols,) or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous bfloat16 tensor of {cols} elements")
+    if residual is not None:
+        _check_bf16_matrix(residual, "residual")
+        if residual.shape != x.shape:
+            raise ValueError(f"residual must have shape {tuple(x.shape)}, got {tuple(residual.shape)}")
+        if residual_out is not None:
+            _check_out_matrix(residual_out, "residual_out", torch.bfloat16, rows, cols)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if codes is not None:
+        _check_codes(codes, "codes", x.shape)
+    if scale is not None:
+        _check_row_scale(scale, "scale", rows)
+    dev = _check_devices(x=x, weight=weight, residual=residual, residual_out=residual_out,
+                         codes=codes, scale=scale)
+    if residual is not None and residual_out is None:
+        residual_out = _empty((rows, cols), torch.bfloat16, dev, stream)
+    if codes is None:
+        codes = _empty((rows, cols), torch.int8, dev, stream)
+    if scale is None:
+        scale = _empty((rows,), torch.float32, dev, stream)
+    has = residual is not None
+    _lib.check("nvfp4_add_rms_norm_int8", _lib.lib().nvfp4_add_rms_norm_int8(
+        x.data_ptr(), _ld(x), residual.data_ptr() if has else 0, _ld(residual) if has else 0,
+        weight.data_ptr(), weight_offset, eps, rows, cols,
+        residual_out.data_ptr() if has else 0, _ld(residual_out) if has else 0,
+        codes.data_ptr(), scale.data_ptr(), _stream(stream)))
+    return Int8Tensor(codes, scale), residual_out
+
+
+def int8_gemm(a: Int8Tensor, w: Int8Tensor, y: Optional[torch.Tensor] = None,
+              stream=None) -> torch.Tensor:
+    """y = a @ w.T in BF16 from int8 codes with a scale per token and per
+    channel, accumulated exactly in 32-bit integers.  An N that is not a
+    multiple of 8 gives a y whose row stride is the next one."""
+    _check_codes(a.codes, "a.codes")
+    _check_codes(w.codes, "w.codes")
+    M, K = a.codes.shape
+    N = w.codes.shape[0]
+    if w.codes.shape[1] != K:
+        raise ValueError("inner dimensions differ")
+    _check_row_scale(a.scale, "a.scale", M)
+    _check_row_scale(w.scale, "w.scale", N)
+    if y is not None:
+        _check_out_matrix(y, "y", torch.bfloat16, M, N)
+    dev = _check_devices(a_codes=a.codes, a_scale=a.scale, w_codes=w.codes, w_scale=w.scale, y=y)
+    if y is None:
+        y = _empty((M, (N + 7) // 8 * 8), torch.bfloat16, dev, stream)
+        if N % 8:
+            y = y[:, :N]
+    _lib.check("nvfp4_int8_gemm", _lib.lib().nvfp4_int8_gemm(
+        a.codes.data_ptr(), a.scale.data_ptr(), w.codes.data_ptr(), w.scale.data_ptr(),
+        y.data_ptr(), _ld(y), M, N, K, _stream(stream)))
+    return y
+
+
+# ---------------------------------------------------------------------------
 # the quantized weight format on disk: quantize (and harmonise) once offline,
 # serve many times.  One torch file holding plain CPU tensors and integers
 # (loadable with weights_only=True): packed codes, scale bytes in their
@@ -574,13 +736,19 @@ _FORMAT_VERSION = 1
 
 
 def save_quantized(path: str, w) -> None:
-    """Write a QuantizedTensor or FusedWeight (device or host tensors) to path."""
+    """Write a QuantizedTensor, FusedWeight or Int8Tensor (device or host
+    tensors) to path."""
+    if isinstance(w, Int8Tensor):
+        torch.save({"format": _FORMAT, "version": _FORMAT_VERSION, "kind": "int8",
+                    "codes": w.codes.detach().to("cpu").contiguous(),
+                    "scale": w.scale.detach().to("cpu").contiguous()}, path)
+        return
     if isinstance(w, FusedWeight):
         kind, sizes, gs, layout = "fused", list(w.sizes), list(w.g_list), SF_TCGEN05
     elif isinstance(w, QuantizedTensor):
         kind, sizes, gs, layout = "single", [w.rows], [w.g], w.layout
     else:
-        raise TypeError("save_quantized takes a QuantizedTensor or a FusedWeight")
+        raise TypeError("save_quantized takes a QuantizedTensor, a FusedWeight or an Int8Tensor")
     g = torch.cat([t.detach().reshape(-1)[:1].to("cpu", torch.float32) for t in gs])
     torch.save({"format": _FORMAT, "version": _FORMAT_VERSION, "kind": kind,
                 "rows": int(sum(sizes)), "cols": int(w.cols), "layout": int(layout),
@@ -596,6 +764,13 @@ def load_quantized(path: str, device="cuda"):
     d = torch.load(path, map_location="cpu", weights_only=True)
     if not isinstance(d, dict) or d.get("format") != _FORMAT or d.get("version") != _FORMAT_VERSION:
         raise ValueError(f"{path}: not an {_FORMAT} v{_FORMAT_VERSION} file")
+    if d.get("kind") == "int8":
+        _check_codes(d["codes"], "codes")
+        _check_row_scale(d["scale"], "scale", d["codes"].shape[0])
+        if d["codes"].shape[1] % 16 or not bool(torch.isfinite(d["scale"]).all()) or \
+                not bool((d["scale"] > 0).all()):
+            raise ValueError(f"{path}: inconsistent int8 weight")
+        return Int8Tensor(d["codes"].to(device), d["scale"].to(device))
     rows, cols, layout, sizes = d["rows"], d["cols"], d["layout"], d["sizes"]
     if layout not in (SF_LINEAR, SF_TCGEN05) or cols % 32 or sum(sizes) != rows or \
             any(n <= 0 for n in sizes) or d["kind"] not in ("single", "fused"):

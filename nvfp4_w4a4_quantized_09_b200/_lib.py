@@ -31,6 +31,7 @@ NOALLOC_SCRATCH_BYTES = 256
 P = ctypes.c_void_p
 I64 = ctypes.c_int64
 I32 = ctypes.c_int
+F32 = ctypes.c_float
 ST = ctypes.c_int
 
 
@@ -64,6 +65,9 @@ SIGNATURES = {
     "nvfp4_harmonize_scales": (ST, [P, I64, ctypes.POINTER(Segment), I32, I32, P, P]),
     "nvfp4_kv_scale_from_amax": (ST, [P, P, P]),
     "nvfp4_kv_quantize_e4m3": (ST, [P, I64, I64, I64, P, P, I64, P]),
+    "nvfp4_int8_quantize": (ST, [P, I64, I64, I64, P, P, P]),
+    "nvfp4_add_rms_norm_int8": (ST, [P, I64, P, I64, P, F32, F32, I64, I64, P, I64, P, P, P]),
+    "nvfp4_int8_gemm": (ST, [P, P, P, P, P, I64, I64, I64, I64, P]),
     "nvfp4_last_device_status": (ST, [P]),
     "nvfp4_debug_wait_timeout": (ST, [I64, P]),
     "nvfp4_status_string": (ctypes.c_char_p, [ST]),
