@@ -6,20 +6,389 @@
 //
 // K is at most 131056, so |acc| <= 128 * 128 * K < 2^31: the sum cannot
 // overflow, and integer addition gives the same bits in any order.  Tile sizes
-// and splits of K are therefore free choices that no result depends on.
+// and splits of K are therefore free choices that no result depends on; both
+// kernels and every configuration of them give the same bits.
+//
+//   M <= 256   int8_gemm_few_kernel (int8_gemm_few.cuh): operands swapped, the
+//              weight streamed once, K split over a cluster.
+//   M > 256    int8_gemm_pair_kernel: a CTA pair per 256 x BN tile.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "host_common.h"
+#include "int8_mma.cuh"
 #include "nvfp4.h"
+#include "ptx.cuh"
 
 namespace nvfp4 {
 namespace {
 
 constexpr int64_t kMaxK = 131056;
+constexpr int kRows = 128;                      // rows of an operand tile per CTA
+constexpr int kStepBytes = 128;                 // values of K per pipeline stage
+constexpr uint64_t kTimeoutNs = 1000000000ull;  // 1 s per wait
 
-struct Int8GemmArgs {
+// The product's value: the sum rounded to binary32, both scales, BF16 bits.
+__device__ __forceinline__ float scale_f32(int32_t acc, float sa, float sw) {
+    return __fmul_rn(__fmul_rn(__int2float_rn(acc), sa), sw);
+}
+__device__ __forceinline__ uint16_t scale_bf16(int32_t acc, float sa, float sw) {
+    return __bfloat16_as_ushort(__float2bfloat16_rn(scale_f32(acc, sa, sw)));
+}
+
+#include "int8_gemm_few.cuh"
+
+// ---------------------------------------------------------------------------
+// CTA-pair kernel (cta_group::2).  A cluster of two CTAs on two SMs computes a
+// 256 x BN tile (BN a multiple of 32 up to 256, chosen by the launcher so that
+// the tiles fill whole rounds of the pairs): each CTA loads its 128 rows of A
+// and its BN / 2 rows of W per k-step of 128, the even CTA issues the MMAs
+// (M = 256, N = BN, K = 32), accumulator rows 0..127 live in the even CTA's
+// TMEM and 128..255 in the odd one's.  Two accumulators of 256 columns each:
+// the epilogue drains one while the MMAs fill the other.
+//   warp 0      TMA producer (both CTAs; bytes counted on the even CTA's barrier)
+//   warp 1      MMA issuer (even CTA), TMEM owner
+//   warps 2..9  epilogue: two warps per TMEM lane quarter take alternate
+//               32-column chunks: scales, BF16, a 32 x 32 tile staged in the
+//               64-byte swizzle and one TMA store of it (rows beyond M and
+//               whole 16-byte pieces beyond N clipped by the tensor map)
+// ---------------------------------------------------------------------------
+constexpr int kPairThreads = 320;
+constexpr int kEpiWarps = 8;
+constexpr int kPairMaxStages = 8;
+constexpr int kPairMaxBN = 256;
+constexpr int kEpiBytes = 32 * 64;              // one staged 32 x 32 BF16 tile
+constexpr int kEpiBufs = 2;
+constexpr uint32_t kPairEpi = kEpiWarps * kEpiBufs * kEpiBytes;
+constexpr uint32_t kPairBars = (2 * kPairMaxStages + 5) * 8;
+constexpr uint32_t kPairSmem = 227 * 1024;      // whole: one CTA per SM
+constexpr uint32_t kPairRing = (kPairSmem - 1024 - kPairEpi - kPairBars - 16) / 1024 * 1024;
+
+struct PairArgs {
+    const float* sa;
+    const float* sw;
+    uint16_t* y;
+    int64_t ldy;
+    int M, N, K;
+    int m_tiles, n_tiles, k_steps;
+    int group_m;                                // raster: m-tiles visited per n sweep
+    int bn;                                     // tile width
+    int stages;
+    uint64_t timeout_ns;
+    int* status;
+};
+
+__host__ __device__ constexpr uint32_t pair_stage_bytes(int bn) {
+    return static_cast<uint32_t>(kRows + bn / 2) * kStepBytes;
+}
+__host__ __device__ constexpr int pair_stages(int bn) {
+    return static_cast<int>(kPairRing / pair_stage_bytes(bn)) < kPairMaxStages
+               ? static_cast<int>(kPairRing / pair_stage_bytes(bn)) : kPairMaxStages;
+}
+static_assert(pair_stages(256) >= 5, "the widest tile keeps a deep ring");
+static_assert(kPairSmem > 228 * 1024 / 2, "two CTAs could share an SM and its 512 TMEM columns");
+
+__device__ __forceinline__ void pair_tile(int t, const PairArgs& a, int& mt, int& nt) {
+    const int group_m = min(a.group_m, a.m_tiles);
+    const int per_group = group_m * a.n_tiles;
+    const int grp = t / per_group;
+    const int first_m = grp * group_m;
+    const int gsize = min(group_m, a.m_tiles - first_m);
+    const int local = t - grp * per_group;
+    mt = first_m + local % gsize;
+    nt = local / gsize;
+}
+
+__global__ void __launch_bounds__(kPairThreads, 1)
+int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
+                      const __grid_constant__ CUtensorMap tmap_b,
+                      const __grid_constant__ CUtensorMap tmap_y, const PairArgs args) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int STAGES = args.stages;
+    const int BN = args.bn;
+    constexpr uint32_t A_BYTES = kRows * kStepBytes;
+    const uint32_t B_BYTES = static_cast<uint32_t>(BN / 2) * kStepBytes;
+    const uint32_t off_b = STAGES * A_BYTES;
+    uint8_t* epi = smem + kPairRing;
+    uint64_t* full = reinterpret_cast<uint64_t*>(epi + kPairEpi);
+    uint64_t* empty = full + kPairMaxStages;
+    uint64_t* tmem_full = empty + kPairMaxStages;       // [2]
+    uint64_t* tmem_empty = tmem_full + 2;               // [2]
+    uint64_t* drain = tmem_empty + 2;
+    uint32_t* s_tmem_base = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem_base + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();             // 0: issues the pair's MMAs
+    const int pair = blockIdx.x >> 1;
+    const int npairs = gridDim.x >> 1;
+    const int total_tiles = args.m_tiles * args.n_tiles;
+    grid_launch_dependents();
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tmem_full[i], 1);
+            mbar_init(&tmem_empty[i], 2 * kEpiWarps);    // both CTAs' epilogue warps
+        }
+        mbar_init(drain, 1);
+        *s_abort = 0;
+        fence_mbar_init();
+        prefetch_tmap(&tmap_a);
+        prefetch_tmap(&tmap_b);
+        prefetch_tmap(&tmap_y);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(s_tmem_base, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                                      // barriers of both CTAs initialised
+    tc_fence_after();
+    const uint32_t tmem_base = *s_tmem_base;
+    const uint32_t full0_leader = mapa_shared(smem_u32(&full[0]), 0);
+    const uint32_t tmem_empty_leader = mapa_shared(smem_u32(tmem_empty), 0);
+
+    if (warp == 0) {
+        // ---------------- TMA producer (both CTAs) ----------------
+        grid_dependency_wait();
+        const uint64_t pol = l2_policy_evict_last();
+        int stage = 0;
+        uint32_t phase = 0;
+        uint32_t armed = 0, armed_parity = 0;   // stages the even CTA expects bytes on
+        bool ok = true;
+        for (int t = pair; t < total_tiles && ok; t += npairs) {
+            int mt, nt;
+            pair_tile(t, args, mt, nt);
+            for (int kb = 0; kb < args.k_steps; ++kb) {
+                if (!mbar_wait_warp_pipe(&empty[stage], phase ^ 1u, args.timeout_ns, s_abort, args.status)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t fb = full0_leader + stage * 8;
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (A_BYTES + B_BYTES));
+                    tma_load_2d_pair(smem + stage * A_BYTES, &tmap_a, fb, kb * kStepBytes,
+                                     mt * 256 + static_cast<int>(rank) * kRows, pol);
+                    tma_load_2d_pair(smem + off_b + stage * B_BYTES, &tmap_b, fb, kb * kStepBytes,
+                                     nt * BN + static_cast<int>(rank) * (BN / 2), pol);
+                }
+                __syncwarp();
+                if (rank == 0) {
+                    armed |= 1u << stage;
+                    armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+                }
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (!ok && rank == 0 && lane == 0) {
+            // leave no copy of either CTA in flight on the stages armed here
+            int local_abort = 0;
+            for (int s = 0; s < STAGES; ++s)
+                if (armed & (1u << s))
+                    mbar_wait_bounded(&full[s], (armed_parity >> s) & 1u, args.timeout_ns,
+                                      &local_abort, args.status);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0) {
+            // ---------------- MMA issuer (even CTA) ----------------
+            const uint32_t idesc = int8_idesc(256, BN);
+            const uint64_t da0 = sdesc_kmajor_sw128(smem_u32(smem));
+            const uint64_t db0 = sdesc_kmajor_sw128(smem_u32(smem + off_b));
+            const int last_kb = args.k_steps - 1;
+            const int last_n = (args.K - last_kb * kStepBytes + 31) / 32;   // MMAs of the last k-step
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true;
+            for (int t = pair; t < total_tiles && ok; t += npairs) {
+                if (!mbar_wait_warp(&tmem_empty[acc], acc_phase ^ 1u, args.timeout_ns, s_abort, args.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + acc * 256;
+                for (int kb = 0; kb < args.k_steps; ++kb) {
+                    if (!mbar_wait_warp_pipe(&full[stage], phase, args.timeout_ns, s_abort, args.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    // descriptor start addresses advance by 2 per 32 bytes of K
+                    const uint64_t da = da0 + static_cast<uint64_t>(stage * (A_BYTES / 16));
+                    const uint64_t db = db0 + static_cast<uint64_t>(stage * (B_BYTES / 16));
+                    const uint32_t first = kb != 0;
+                    const int nmma = kb == last_kb ? last_n : kStepBytes / 32;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int j = 0; j < kStepBytes / 32; ++j)
+                            if (j < nmma)
+                                tc_mma_i8_pair(d_tmem, da + 2 * j, db + 2 * j, idesc,
+                                               first | static_cast<uint32_t>(j));
+                        tc_commit_pair(&empty[stage], 0x3);
+                    }
+                    __syncwarp();
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok && elect_one()) tc_commit_pair(&tmem_full[acc], 0x3);
+                __syncwarp();
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+            // every tcgen05 operation issued above has finished before TMEM is freed
+            if (elect_one()) {
+                tc_commit_pair(drain, 0x1);
+                int local_abort = 0;
+                mbar_wait_bounded(drain, 0, args.timeout_ns, &local_abort, args.status);
+            }
+            __syncwarp();
+        }
+    } else {
+        // ---------------- epilogue (warps 2..9, both CTAs) ----------------
+        grid_dependency_wait();
+        const int q = warp & 3;
+        const int half = (warp - 2) >> 2;
+        const uint64_t pol_y = l2_policy_evict_first();
+        uint8_t* stage_y = epi + (warp - 2) * (kEpiBufs * kEpiBytes);
+        const uint32_t swz = static_cast<uint32_t>((lane >> 1) & 3);
+        const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+        int acc = 0, buf = 0;
+        uint32_t acc_phase = 0;
+        for (int t = pair; t < total_tiles; t += npairs) {
+            int mt, nt;
+            pair_tile(t, args, mt, nt);
+            const int m0 = mt * 256 + static_cast<int>(rank) * kRows + q * 32;   // row of lane 0
+            const float sa = m0 + lane < args.M ? args.sa[m0 + lane] : 0.0f;
+            if (!mbar_wait_warp(&tmem_full[acc], acc_phase, args.timeout_ns, s_abort, args.status)) break;
+            tc_fence_after();
+            if (m0 < args.M) {                                         // warp-uniform
+                for (int c = half * 32; c < BN; c += 64) {
+                    const int n0 = nt * BN + c;
+                    if (n0 >= args.N) break;                           // warp-uniform
+                    const float swl = n0 + lane < args.N ? args.sw[n0 + lane] : 0.0f;
+                    uint32_t r[32];
+                    tmem_ld_32cols(tq + acc * 256 + c, r);
+                    tmem_ld_wait();
+                    uint32_t o[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float v0 = scale_f32(static_cast<int32_t>(r[2 * j]), sa,
+                                                   __shfl_sync(0xFFFFFFFFu, swl, 2 * j));
+                        const float v1 = scale_f32(static_cast<int32_t>(r[2 * j + 1]), sa,
+                                                   __shfl_sync(0xFFFFFFFFu, swl, 2 * j + 1));
+                        o[j] = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(v0))) |
+                               (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(v1))) << 16);
+                    }
+                    if (n0 + 32 > args.N && (args.N & 7) != 0) {       // warp-uniform
+                        // TMA stores whole 16-byte pieces of a row: columns
+                        // that end inside one are stored from here
+                        if (m0 + lane < args.M) {
+                            uint16_t* yp = args.y + static_cast<int64_t>(m0 + lane) * args.ldy + n0;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (n0 + j < args.N)
+                                    yp[j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
+                        }
+                        continue;
+                    }
+                    // the store that last used this buffer has finished reading it
+                    uint8_t* sb = stage_y + buf * kEpiBytes;
+                    const uint32_t sy = smem_u32(sb);
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                    __syncwarp();
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        sts128(sy + lane * 64 + ((static_cast<uint32_t>(u) ^ swz) << 4), o[4 * u],
+                               o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&tmap_y, sb, n0, m0, pol_y);
+                        bulk_commit_group();
+                    }
+                    buf ^= 1;
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(tmem_empty_leader + acc * 8);
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+        // every store of this warp has completed before the CTA exits
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                                      // no CTA leaves while its peer may signal it
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                             CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                             CUtensorMapFloatOOBfill);
+
+// Looked up once (a thread-safe local static); nullptr when the driver has none.
+EncodeFn tensor_map_encoder() {
+    static const EncodeFn fn = []() -> EncodeFn {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<EncodeFn>(p);
+        return nullptr;
+    }();
+    return fn;
+}
+
+// 2-D map of a [rows, cols] matrix, row stride in bytes; zero fill (loads) and
+// clipping (stores) beyond it.
+bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64_t rows, int64_t cols,
+              int64_t stride_bytes, int box_cols, int box_rows, CUtensorMapSwizzle swizzle,
+              CUtensorMapL2promotion promo) {
+    const EncodeFn fn = tensor_map_encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride_bytes)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              swizzle, promo, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_codes_map(CUtensorMap* m, const int8_t* base, int64_t rows, int64_t K, int box_rows) {
+    return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, rows, K, K, kStepBytes, box_rows,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+struct Operands {
     const int8_t* a;
     const int8_t* w;
     const float* sa;
@@ -29,52 +398,122 @@ struct Int8GemmArgs {
     int M, N, K;
 };
 
-// 64 x 64 outputs per CTA, 4 x 4 per thread, four products per dp4a.
-constexpr int kTile = 64;
-constexpr int kStep = 64;      // bytes of K per step
+// The launches are programmatic dependents: the kernels wait for the previous
+// grid before they touch global memory, so only their set-up overlaps it.
+void launch_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2], int cluster, int threads,
+                   uint32_t smem, cudaStream_t stream) {
+    *cfg = {};
+    cfg->blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg->dynamicSmemBytes = smem;
+    cfg->stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg->attrs = attr;
+    cfg->numAttrs = 2;
+}
 
-__global__ void __launch_bounds__(256) int8_gemm_kernel(const Int8GemmArgs g) {
-    __shared__ int32_t as[kTile][kStep / 4 + 1], ws[kTile][kStep / 4 + 1];
-    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kTile, n0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    int acc[4][4] = {};
-    const int lr = threadIdx.x >> 2, lc = (threadIdx.x & 3) * 16;
-    for (int k0 = 0; k0 < g.K; k0 += kStep) {
-        int4 av = make_int4(0, 0, 0, 0), wv = av;
-        if (k0 + lc < g.K) {
-            if (m0 + lr < g.M) av = *reinterpret_cast<const int4*>(g.a + (m0 + lr) * g.K + k0 + lc);
-            if (n0 + lr < g.N) wv = *reinterpret_cast<const int4*>(g.w + (n0 + lr) * g.K + k0 + lc);
+nvfp4_status launch_few(const Operands& o, int* status, cudaStream_t stream) {
+    auto kern = int8_gemm_few_kernel;
+    static PerDeviceOnce once;
+    static int slots[kMaxDevices][kFewMaxSplit + 1];   // resident clusters per split
+    int dev = 0;
+    nvfp4_status st = current_device(&dev);
+    if (st != NVFP4_OK) return st;
+    st = once.run(dev, [&] {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
+            cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
+            return NVFP4_ERR_CUDA;
+        for (int s = 1; s <= kFewMaxSplit; ++s) {
+            cudaLaunchConfig_t cfg;
+            cudaLaunchAttribute attr[2];
+            launch_config(&cfg, attr, s, kFewThreads, 227 * 1024, nullptr);
+            cfg.numAttrs = 1;            // the occupancy query takes the cluster shape only
+            cfg.gridDim = dim3(static_cast<unsigned>(s), 1, 1);
+            if (cudaOccupancyMaxActiveClusters(&slots[dev][s], kern, &cfg) != cudaSuccess || slots[dev][s] <= 0)
+                return NVFP4_ERR_CUDA;
         }
-        __syncthreads();
-        as[lr][lc / 4] = av.x, as[lr][lc / 4 + 1] = av.y, as[lr][lc / 4 + 2] = av.z, as[lr][lc / 4 + 3] = av.w;
-        ws[lr][lc / 4] = wv.x, ws[lr][lc / 4 + 1] = wv.y, ws[lr][lc / 4 + 2] = wv.z, ws[lr][lc / 4 + 3] = wv.w;
-        __syncthreads();
-        for (int k = 0; k < kStep / 4; ++k) {
-            int a4[4], w4[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                a4[i] = as[ty + 16 * i][k];
-                w4[i] = ws[tx + 16 * i][k];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(a4[i], w4[j], acc[i][j]);
-        }
+        return NVFP4_OK;
+    });
+    if (st != NVFP4_OK) return st;
+
+    FewArgs f = {};
+    f.sa = o.sa, f.sw = o.sw, f.y = o.y, f.ldy = o.ldy, f.M = o.M, f.N = o.N, f.K = o.K;
+    f.nt = (o.M + 15) / 16 * 16;
+    f.n_tiles = (o.N + kRows - 1) / kRows;
+    f.k_steps = (o.K + kStepBytes - 1) / kStepBytes;
+    f.timeout_ns = kTimeoutNs;
+    f.status = status;
+    // the split whose rounds of tiles take the fewest k-steps, an exchange of
+    // partial sums counted as a few
+    int best = 0;
+    for (int s = 1; s <= kFewMaxSplit && s <= f.k_steps; ++s) {
+        const int rounds = (f.n_tiles + slots[dev][s] - 1) / slots[dev][s];
+        const int cost = rounds * ((f.k_steps + s - 1) / s + (s > 1 ? 1 + f.nt / 32 : 0));
+        if (best == 0 || cost < best) best = cost, f.split = s;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + ty + 16 * i;
-        if (m >= g.M) continue;
-        const float sa = g.sa[m];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t n = n0 + tx + 16 * j;
-            if (n >= g.N) continue;
-            const float v = __fmul_rn(__fmul_rn(__int2float_rn(acc[i][j]), sa), g.sw[n]);
-            g.y[m * g.ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-        }
+    few_config(f.nt, f.split, &f.stages, &f.nparts, &f.nacc);
+    const int clusters = std::min(f.n_tiles, slots[dev][f.split]);
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    launch_config(&cfg, attr, f.split, kFewThreads, few_layout(f.nt, f.split, f.stages, f.nparts).bytes, stream);
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * f.split), 1, 1);
+    CUtensorMap tw, tx;
+    if (!make_codes_map(&tw, o.w, o.N, o.K, kRows) || !make_codes_map(&tx, o.a, o.M, o.K, f.nt))
+        return NVFP4_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kern, tw, tx, f) != cudaSuccess) return NVFP4_ERR_CUDA;
+    return cuda_status(cudaGetLastError());
+}
+
+nvfp4_status launch_pair(const Operands& o, const DeviceInfo& info, int* status, cudaStream_t stream) {
+    auto kern = int8_gemm_pair_kernel;
+    static PerDeviceOnce once;
+    int dev = 0;
+    nvfp4_status st = current_device(&dev);
+    if (st != NVFP4_OK) return st;
+    st = once.run(dev, [&] {
+        return cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem));
+    });
+    if (st != NVFP4_OK) return st;
+    PairArgs p = {};
+    p.sa = o.sa, p.sw = o.sw, p.y = o.y, p.ldy = o.ldy, p.M = o.M, p.N = o.N, p.K = o.K;
+    p.m_tiles = (o.M + 255) / 256;
+    p.k_steps = (o.K + kStepBytes - 1) / kStepBytes;
+    p.timeout_ns = kTimeoutNs;
+    p.status = status;
+    const int max_pairs = info.sms / 2;
+    // Tile width: a k-step of a tile costs the larger of its MMA time (2 BN
+    // cycles) and its feed ((128 + BN / 2) rows of 128 bytes at about 70 bytes
+    // per cycle and SM); take the width whose rounds of tiles cost least, the
+    // widest among equals.
+    int64_t best = 0;
+    for (int bn = kPairMaxBN; bn >= 64; bn -= 32) {
+        const int64_t tiles = static_cast<int64_t>(p.m_tiles) * ((o.N + bn - 1) / bn);
+        const int64_t step = std::max(2 * bn, static_cast<int>(pair_stage_bytes(bn)) / 70);
+        const int64_t cost = (tiles + max_pairs - 1) / max_pairs * step;
+        if (best == 0 || cost < best) best = cost, p.bn = bn;
     }
+    p.n_tiles = (o.N + p.bn - 1) / p.bn;
+    p.stages = pair_stages(p.bn);
+    // Raster: when A fits comfortably in L2, sweep every M tile for each N tile
+    // (the weight then streams from HBM once); otherwise bands of 16 M tiles.
+    p.group_m = static_cast<int64_t>(o.M) * o.K <= (int64_t(48) << 20) ? 1 << 30 : 16;
+    const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
+    const int pairs = static_cast<int>(std::min<int64_t>(tiles, max_pairs));
+    CUtensorMap ta, tb, ty;
+    if (!make_codes_map(&ta, o.a, o.M, o.K, kRows) || !make_codes_map(&tb, o.w, o.N, o.K, p.bn / 2) ||
+        !make_map(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, o.y, o.M, o.N, o.ldy * 2, 32, 32,
+                  CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE))
+        return NVFP4_ERR_CUDA;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    launch_config(&cfg, attr, 2, kPairThreads, kPairSmem, stream);
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
+    if (cudaLaunchKernelEx(&cfg, kern, ta, tb, ty, p) != cudaSuccess) return NVFP4_ERR_CUDA;
+    return cuda_status(cudaGetLastError());
 }
 
 }  // namespace
@@ -87,11 +526,14 @@ extern "C" nvfp4_status nvfp4_int8_gemm(const int8_t* a_codes, const float* a_sc
                                         int64_t ldy, int64_t M, int64_t N, int64_t K, void* stream) {
     if (M < 0 || N < 0 || K < 0) return NVFP4_ERR_INVALID_ARG;
     if (K % 16 != 0 || K < 16 || K > kMaxK) return NVFP4_ERR_UNSUPPORTED_SHAPE;
-    if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    // tile indices and row numbers are 32-bit in the kernels; a tile's rows may
+    // pass the last one by less than 512, a walk over the tiles by the grid
+    constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1024;
+    if (M > kMaxDim || N > kMaxDim) return NVFP4_ERR_UNSUPPORTED_SHAPE;
     if (M == 0 || N == 0) return NVFP4_OK;
     if (ldy < N || ldy % 8 != 0) return NVFP4_ERR_ALIGNMENT;
     if (extent_too_large(M, ldy, 2)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
-    if (((M + 127) / 128) * ((N + 127) / 128) >= (int64_t(1) << 30)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (((M + 127) / 128) * ((N + 63) / 64) >= (int64_t(1) << 30)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
     if (!a_codes || !a_scale || !w_codes || !w_scale || !y) return NVFP4_ERR_INVALID_ARG;
     if (!aligned16(a_codes) || !aligned16(w_codes) || !aligned16(y) ||
         (reinterpret_cast<uintptr_t>(a_scale) & 3u) != 0 || (reinterpret_cast<uintptr_t>(w_scale) & 3u) != 0)
@@ -103,13 +545,13 @@ extern "C" nvfp4_status nvfp4_int8_gemm(const int8_t* a_codes, const float* a_sc
         overlaps(a_scale, static_cast<size_t>(M) * 4, y, yb) ||
         overlaps(w_scale, static_cast<size_t>(N) * 4, y, yb))
         return NVFP4_ERR_INVALID_ARG;
-    DeviceInfo dev;
-    const nvfp4_status st = require_sm100(&dev);
+    DeviceInfo info;
+    const nvfp4_status st = require_sm100(&info);
     if (st != NVFP4_OK) return st;
-    Int8GemmArgs g = {a_codes, w_codes, a_scale, w_scale, static_cast<uint16_t*>(y), ldy,
-                      static_cast<int>(M), static_cast<int>(N), static_cast<int>(K)};
-    const dim3 grid(static_cast<unsigned>((N + kTile - 1) / kTile), static_cast<unsigned>((M + kTile - 1) / kTile));
-    if (grid.y > 65535) return NVFP4_ERR_UNSUPPORTED_SHAPE;
-    int8_gemm_kernel<<<grid, 256, 0, as_stream(stream)>>>(g);
-    return cuda_status(cudaGetLastError());
+    int* status = device_status_ptr();
+    if (!status) return NVFP4_ERR_CUDA;
+    const Operands o = {a_codes, w_codes, a_scale, w_scale, static_cast<uint16_t*>(y), ldy,
+                        static_cast<int>(M), static_cast<int>(N), static_cast<int>(K)};
+    return M <= kFewMaxTokens ? launch_few(o, status, as_stream(stream))
+                              : launch_pair(o, info, status, as_stream(stream));
 }
