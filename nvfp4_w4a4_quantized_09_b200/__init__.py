@@ -604,17 +604,35 @@ def _ld(t: torch.Tensor) -> int:
     return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
 
 
-def _empty(shape, dtype, device, stream):
+def _empty(*shape, dtype, device, stream):
     """torch.empty for a kernel on `stream`: with an explicit stream the memory
     is that stream's, so that no earlier use of it on another one can still be
     running, and it is kept from reuse until the current stream is done with
     it as well."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = torch.empty(*shape, dtype=dtype, device=device)
     t.record_stream(torch.cuda.current_stream(device))
     return t
+
+
+# The calls below take a few microseconds on the device for a decode step, so
+# the checks of a correct call are kept to plain attribute reads: the device by
+# its index, the stream by its handle.
+def _on_current_device(names, tensors) -> torch.device:
+    index = tensors[0].get_device()
+    same = index >= 0 and index == torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            same = False
+    if not same:
+        _check_devices(**dict(zip(names, tensors)))          # raises, naming the tensor
+    return tensors[0].device
+
+
+def _stream_handle(device: torch.device, stream) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def _check_codes(t, name: str, shape=None):
@@ -640,13 +658,15 @@ def int8_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
         _check_codes(codes, "codes", x.shape)
     if scale is not None:
         _check_row_scale(scale, "scale", rows)
-    dev = _check_devices(x=x, codes=codes, scale=scale)
+    dev = _on_current_device(("x", "codes", "scale"), (x, codes, scale))
     if codes is None:
-        codes = _empty((rows, cols), torch.int8, dev, stream)
+        codes = _empty(rows, cols, dtype=torch.int8, device=dev, stream=stream)
     if scale is None:
-        scale = _empty((rows,), torch.float32, dev, stream)
-    _lib.check("nvfp4_int8_quantize", _lib.lib().nvfp4_int8_quantize(
-        x.data_ptr(), rows, cols, _ld(x), codes.data_ptr(), scale.data_ptr(), _stream(stream)))
+        scale = _empty(rows, dtype=torch.float32, device=dev, stream=stream)
+    st = _lib.lib().nvfp4_int8_quantize(x.data_ptr(), rows, cols, _ld(x), codes.data_ptr(),
+                                        scale.data_ptr(), _stream_handle(dev, stream))
+    if st:
+        raise Nvfp4Error("nvfp4_int8_quantize", st)
     return codes, scale
 
 
@@ -682,20 +702,22 @@ def add_rms_norm_int8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[
         _check_codes(codes, "codes", x.shape)
     if scale is not None:
         _check_row_scale(scale, "scale", rows)
-    dev = _check_devices(x=x, weight=weight, residual=residual, residual_out=residual_out,
-                         codes=codes, scale=scale)
-    if residual is not None and residual_out is None:
-        residual_out = _empty((rows, cols), torch.bfloat16, dev, stream)
+    dev = _on_current_device(("x", "weight", "residual", "residual_out", "codes", "scale"),
+                             (x, weight, residual, residual_out, codes, scale))
     if codes is None:
-        codes = _empty((rows, cols), torch.int8, dev, stream)
+        codes = _empty(rows, cols, dtype=torch.int8, device=dev, stream=stream)
     if scale is None:
-        scale = _empty((rows,), torch.float32, dev, stream)
-    has = residual is not None
-    _lib.check("nvfp4_add_rms_norm_int8", _lib.lib().nvfp4_add_rms_norm_int8(
-        x.data_ptr(), _ld(x), residual.data_ptr() if has else 0, _ld(residual) if has else 0,
-        weight.data_ptr(), weight_offset, eps, rows, cols,
-        residual_out.data_ptr() if has else 0, _ld(residual_out) if has else 0,
-        codes.data_ptr(), scale.data_ptr(), _stream(stream)))
+        scale = _empty(rows, dtype=torch.float32, device=dev, stream=stream)
+    r = ldr = out = ldo = 0
+    if residual is not None:
+        if residual_out is None:
+            residual_out = _empty(rows, cols, dtype=torch.bfloat16, device=dev, stream=stream)
+        r, ldr, out, ldo = residual.data_ptr(), _ld(residual), residual_out.data_ptr(), _ld(residual_out)
+    st = _lib.lib().nvfp4_add_rms_norm_int8(
+        x.data_ptr(), _ld(x), r, ldr, weight.data_ptr(), weight_offset, eps, rows, cols, out, ldo,
+        codes.data_ptr(), scale.data_ptr(), _stream_handle(dev, stream))
+    if st:
+        raise Nvfp4Error("nvfp4_add_rms_norm_int8", st)
     return Int8Tensor(codes, scale), residual_out
 
 
@@ -704,24 +726,26 @@ def int8_gemm(a: Int8Tensor, w: Int8Tensor, y: Optional[torch.Tensor] = None,
     """y = a @ w.T in BF16 from int8 codes with a scale per token and per
     channel, accumulated exactly in 32-bit integers.  An N that is not a
     multiple of 8 gives a y whose row stride is the next one."""
-    _check_codes(a.codes, "a.codes")
-    _check_codes(w.codes, "w.codes")
-    M, K = a.codes.shape
-    N = w.codes.shape[0]
-    if w.codes.shape[1] != K:
+    ac, asc, wc, wsc = a.codes, a.scale, w.codes, w.scale
+    _check_codes(ac, "a.codes")
+    _check_codes(wc, "w.codes")
+    M, K = ac.shape
+    N = wc.shape[0]
+    if wc.shape[1] != K:
         raise ValueError("inner dimensions differ")
-    _check_row_scale(a.scale, "a.scale", M)
-    _check_row_scale(w.scale, "w.scale", N)
+    _check_row_scale(asc, "a.scale", M)
+    _check_row_scale(wsc, "w.scale", N)
     if y is not None:
         _check_out_matrix(y, "y", torch.bfloat16, M, N)
-    dev = _check_devices(a_codes=a.codes, a_scale=a.scale, w_codes=w.codes, w_scale=w.scale, y=y)
+    dev = _on_current_device(("a_codes", "a_scale", "w_codes", "w_scale", "y"), (ac, asc, wc, wsc, y))
     if y is None:
-        y = _empty((M, (N + 7) // 8 * 8), torch.bfloat16, dev, stream)
+        y = _empty(M, (N + 7) // 8 * 8, dtype=torch.bfloat16, device=dev, stream=stream)
         if N % 8:
             y = y[:, :N]
-    _lib.check("nvfp4_int8_gemm", _lib.lib().nvfp4_int8_gemm(
-        a.codes.data_ptr(), a.scale.data_ptr(), w.codes.data_ptr(), w.scale.data_ptr(),
-        y.data_ptr(), _ld(y), M, N, K, _stream(stream)))
+    st = _lib.lib().nvfp4_int8_gemm(ac.data_ptr(), asc.data_ptr(), wc.data_ptr(), wsc.data_ptr(),
+                                    y.data_ptr(), _ld(y), M, N, K, _stream_handle(dev, stream))
+    if st:
+        raise Nvfp4Error("nvfp4_int8_gemm", st)
     return y
 
 

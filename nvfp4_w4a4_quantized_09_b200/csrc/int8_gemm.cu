@@ -9,9 +9,9 @@
 // and splits of K are therefore free choices that no result depends on; both
 // kernels and every configuration of them give the same bits.
 //
-//   M <= 256   int8_gemm_few_kernel (int8_gemm_few.cuh): operands swapped, the
-//              weight streamed once, K split over a cluster.
-//   M > 256    int8_gemm_pair_kernel: a CTA pair per 256 x BN tile.
+//   M <= 128   int8_gemm_few_kernel (int8_gemm_few.cuh): one CTA per tile of all
+//              tokens x BN channels, the weight streamed once.
+//   M > 128    int8_gemm_pair_kernel: a CTA pair per 256 x BN tile.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -40,6 +40,8 @@ __device__ __forceinline__ uint16_t scale_bf16(int32_t acc, float sa, float sw) 
     return __bfloat16_as_ushort(__float2bfloat16_rn(scale_f32(acc, sa, sw)));
 }
 
+constexpr int kEpiWarps = 8;                    // two per TMEM lane quarter
+
 #include "int8_gemm_few.cuh"
 
 // ---------------------------------------------------------------------------
@@ -58,7 +60,6 @@ __device__ __forceinline__ uint16_t scale_bf16(int32_t acc, float sa, float sw) 
 //               whole 16-byte pieces beyond N clipped by the tensor map)
 // ---------------------------------------------------------------------------
 constexpr int kPairThreads = 320;
-constexpr int kEpiWarps = 8;
 constexpr int kPairMaxStages = 8;
 constexpr int kPairMaxBN = 256;
 constexpr int kEpiBytes = 32 * 64;              // one staged 32 x 32 BF16 tile
@@ -160,6 +161,11 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
     const uint32_t full0_leader = mapa_shared(smem_u32(&full[0]), 0);
     const uint32_t tmem_empty_leader = mapa_shared(smem_u32(tmem_empty), 0);
 
+    // The two feeding roles run as whole warps with one lane issuing.  A
+    // wait that gives up raises `failed`; from then on the role's waits return
+    // at once and it issues nothing.
+    const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+    const bool leader = elect_one();
     if (warp == 0) {
         // ---------------- TMA producer (both CTAs) ----------------
         grid_dependency_wait();
@@ -167,35 +173,35 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
         int stage = 0;
         uint32_t phase = 0;
         uint32_t armed = 0, armed_parity = 0;   // stages the even CTA expects bytes on
-        bool ok = true;
-        for (int t = pair; t < total_tiles && ok; t += npairs) {
+        bool failed = false, ready = true;      // the ring starts empty
+        for (int t = pair; t < total_tiles; t += npairs) {
             int mt, nt;
             pair_tile(t, args, mt, nt);
+            const int ya = mt * 256 + static_cast<int>(rank) * kRows;
+            const int yb = nt * BN + static_cast<int>(rank) * (BN / 2);
             for (int kb = 0; kb < args.k_steps; ++kb) {
-                if (!mbar_wait_warp_pipe(&empty[stage], phase ^ 1u, args.timeout_ns, s_abort, args.status)) {
-                    ok = false;
-                    break;
-                }
+                if (!ready) failed |= !mbar_spin(empty0 + 8 * stage, phase ^ 1u, failed ? 1 : kSpinTries);
+                const int next = stage + 1 == STAGES ? 0 : stage + 1;
+                const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
+                ready = mbar_peek(empty0 + 8 * next, next_phase ^ 1u);
                 const uint32_t fb = full0_leader + stage * 8;
-                if (elect_one()) {
+                if (leader && !failed) {
                     if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (A_BYTES + B_BYTES));
-                    tma_load_2d_pair(smem + stage * A_BYTES, &tmap_a, fb, kb * kStepBytes,
-                                     mt * 256 + static_cast<int>(rank) * kRows, pol);
-                    tma_load_2d_pair(smem + off_b + stage * B_BYTES, &tmap_b, fb, kb * kStepBytes,
-                                     nt * BN + static_cast<int>(rank) * (BN / 2), pol);
+                    tma_load_2d_pair(smem + stage * A_BYTES, &tmap_a, fb, kb * kStepBytes, ya, pol);
+                    tma_load_2d_pair(smem + off_b + stage * B_BYTES, &tmap_b, fb, kb * kStepBytes, yb, pol);
                 }
                 __syncwarp();
-                if (rank == 0) {
+                if (rank == 0 && !failed) {
                     armed |= 1u << stage;
                     armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
                 }
-                if (++stage == STAGES) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
+                stage = next;
+                phase = next_phase;
             }
         }
-        if (!ok && rank == 0 && lane == 0) {
+        if (__any_sync(0xFFFFFFFFu, failed) && lane == 0) {
+            *s_abort = 1;
+            atomicExch(args.status, kDevTimeout);
             // leave no copy of either CTA in flight on the stages armed here
             int local_abort = 0;
             for (int s = 0; s < STAGES; ++s)
@@ -212,47 +218,46 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             const uint64_t db0 = sdesc_kmajor_sw128(smem_u32(smem + off_b));
             const int last_kb = args.k_steps - 1;
             const int last_n = (args.K - last_kb * kStepBytes + 31) / 32;   // MMAs of the last k-step
+            const uint32_t acc_empty0 = smem_u32(tmem_empty);
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
-            bool ok = true;
-            for (int t = pair; t < total_tiles && ok; t += npairs) {
-                if (!mbar_wait_warp(&tmem_empty[acc], acc_phase ^ 1u, args.timeout_ns, s_abort, args.status)) {
-                    ok = false;
-                    break;
-                }
+            bool failed = false, ready = false;
+            for (int t = pair; t < total_tiles; t += npairs) {
+                failed |= !mbar_spin(acc_empty0 + 8 * acc, acc_phase ^ 1u, failed ? 1 : kSpinTries);
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * 256;
                 for (int kb = 0; kb < args.k_steps; ++kb) {
-                    if (!mbar_wait_warp_pipe(&full[stage], phase, args.timeout_ns, s_abort, args.status)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!ready) failed |= !mbar_spin(full0 + 8 * stage, phase, failed ? 1 : kSpinTries);
                     tc_fence_after();
+                    const int next = stage + 1 == STAGES ? 0 : stage + 1;
+                    const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
+                    ready = mbar_peek(full0 + 8 * next, next_phase);
                     // descriptor start addresses advance by 2 per 32 bytes of K
                     const uint64_t da = da0 + static_cast<uint64_t>(stage * (A_BYTES / 16));
                     const uint64_t db = db0 + static_cast<uint64_t>(stage * (B_BYTES / 16));
-                    const uint32_t first = kb != 0;
                     const int nmma = kb == last_kb ? last_n : kStepBytes / 32;
-                    if (elect_one()) {
+                    if (leader && !failed) {
 #pragma unroll
                         for (int j = 0; j < kStepBytes / 32; ++j)
                             if (j < nmma)
                                 tc_mma_i8_pair(d_tmem, da + 2 * j, db + 2 * j, idesc,
-                                               first | static_cast<uint32_t>(j));
+                                               static_cast<uint32_t>(kb | j));
                         tc_commit_pair(&empty[stage], 0x3);
+                        if (kb == last_kb) tc_commit_pair(&tmem_full[acc], 0x3);
                     }
                     __syncwarp();
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    stage = next;
+                    phase = next_phase;
                 }
-                if (ok && elect_one()) tc_commit_pair(&tmem_full[acc], 0x3);
-                __syncwarp();
                 acc ^= 1;
                 if (acc == 0) acc_phase ^= 1u;
             }
             // every tcgen05 operation issued above has finished before TMEM is freed
+            if (__any_sync(0xFFFFFFFFu, failed) && lane == 0) {
+                *s_abort = 1;
+                atomicExch(args.status, kDevTimeout);
+            }
+            __syncwarp();
             if (elect_one()) {
                 tc_commit_pair(drain, 0x1);
                 int local_abort = 0;
@@ -388,6 +393,24 @@ bool make_codes_map(CUtensorMap* m, const int8_t* base, int64_t rows, int64_t K,
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
+// The same codes as [K / 128][rows][128 bytes], read in boxes of u k-steps: one
+// copy lays u swizzled tiles of 128 bytes a row one behind the other.  Where K
+// is no multiple of 128 the map is [1][rows][K], read a step at a time.
+bool make_steps_map(CUtensorMap* m, const int8_t* base, int64_t rows, int64_t K, int box_rows, int u) {
+    const EncodeFn fn = tensor_map_encoder();
+    if (!fn) return false;
+    const bool whole = K % kStepBytes == 0;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(whole ? kStepBytes : K), static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(whole ? K / kStepBytes : 1)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(whole ? kStepBytes : K)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kStepBytes), static_cast<cuuint32_t>(box_rows),
+                               static_cast<cuuint32_t>(whole ? u : 1)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct Operands {
     const int8_t* a;
     const int8_t* w;
@@ -416,55 +439,45 @@ void launch_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2], int 
     cfg->numAttrs = 2;
 }
 
-nvfp4_status launch_few(const Operands& o, int* status, cudaStream_t stream) {
+nvfp4_status launch_few(const Operands& o, const DeviceInfo& info, int* status, cudaStream_t stream) {
     auto kern = int8_gemm_few_kernel;
     static PerDeviceOnce once;
-    static int slots[kMaxDevices][kFewMaxSplit + 1];   // resident clusters per split
     int dev = 0;
     nvfp4_status st = current_device(&dev);
     if (st != NVFP4_OK) return st;
     st = once.run(dev, [&] {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
-            cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
-            return NVFP4_ERR_CUDA;
-        for (int s = 1; s <= kFewMaxSplit; ++s) {
-            cudaLaunchConfig_t cfg;
-            cudaLaunchAttribute attr[2];
-            launch_config(&cfg, attr, s, kFewThreads, 227 * 1024, nullptr);
-            cfg.numAttrs = 1;            // the occupancy query takes the cluster shape only
-            cfg.gridDim = dim3(static_cast<unsigned>(s), 1, 1);
-            if (cudaOccupancyMaxActiveClusters(&slots[dev][s], kern, &cfg) != cudaSuccess || slots[dev][s] <= 0)
-                return NVFP4_ERR_CUDA;
-        }
-        return NVFP4_OK;
+        return cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem));
     });
     if (st != NVFP4_OK) return st;
-
     FewArgs f = {};
     f.sa = o.sa, f.sw = o.sw, f.y = o.y, f.ldy = o.ldy, f.M = o.M, f.N = o.N, f.K = o.K;
-    f.nt = (o.M + 15) / 16 * 16;
-    f.n_tiles = (o.N + kRows - 1) / kRows;
+    f.nt = (o.M + 7) / 8 * 8;
     f.k_steps = (o.K + kStepBytes - 1) / kStepBytes;
     f.timeout_ns = kTimeoutNs;
     f.status = status;
-    // the split whose rounds of tiles take the fewest k-steps, an exchange of
-    // partial sums counted as a few
-    int best = 0;
-    for (int s = 1; s <= kFewMaxSplit && s <= f.k_steps; ++s) {
-        const int rounds = (f.n_tiles + slots[dev][s] - 1) / slots[dev][s];
-        const int cost = rounds * ((f.k_steps + s - 1) / s + (s > 1 ? 1 + f.nt / 32 : 0));
-        if (best == 0 || cost < best) best = cost, f.split = s;
+    // Tile width: a k-step costs the largest of its MMA time (2 BN cycles), its
+    // feed (128 bytes a row at about 70 bytes per cycle and SM) and the SMs'
+    // common share of memory (about 3400 bytes per cycle); take the width whose
+    // rounds of tiles cost least, the narrowest among equals.
+    int64_t best = 0;
+    for (int bn = 16; bn <= kFewMaxBN; bn += 16) {
+        const int64_t tiles = (o.N + bn - 1) / bn;
+        const int64_t rounds = (tiles + info.sms - 1) / info.sms;
+        const int64_t step = std::max<int64_t>(std::max(2 * bn, (f.nt + bn) * kStepBytes / 70),
+                                               std::min<int64_t>(tiles, info.sms) * bn * kStepBytes / 3400);
+        if (best == 0 || rounds * step < best) best = rounds * step, f.bn = bn;
     }
-    few_config(f.nt, f.split, &f.stages, &f.nparts, &f.nacc);
-    const int clusters = std::min(f.n_tiles, slots[dev][f.split]);
+    f.n_tiles = (o.N + f.bn - 1) / f.bn;
+    few_config(f.nt, f.bn, &f.u, &f.stages);
+    CUtensorMap ta, tw;
+    f.wide = o.K % kStepBytes == 0;
+    if (!make_steps_map(&ta, o.a, o.M, o.K, f.nt, f.u) || !make_steps_map(&tw, o.w, o.N, o.K, f.bn, f.u))
+        return NVFP4_ERR_CUDA;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    launch_config(&cfg, attr, f.split, kFewThreads, few_layout(f.nt, f.split, f.stages, f.nparts).bytes, stream);
-    cfg.gridDim = dim3(static_cast<unsigned>(clusters * f.split), 1, 1);
-    CUtensorMap tw, tx;
-    if (!make_codes_map(&tw, o.w, o.N, o.K, kRows) || !make_codes_map(&tx, o.a, o.M, o.K, f.nt))
-        return NVFP4_ERR_CUDA;
-    if (cudaLaunchKernelEx(&cfg, kern, tw, tx, f) != cudaSuccess) return NVFP4_ERR_CUDA;
+    launch_config(&cfg, attr, 1, kFewThreads, kFewSmem, stream);
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min(f.n_tiles, info.sms)), 1, 1);
+    if (cudaLaunchKernelEx(&cfg, kern, ta, tw, f) != cudaSuccess) return NVFP4_ERR_CUDA;
     return cuda_status(cudaGetLastError());
 }
 
@@ -552,6 +565,6 @@ extern "C" nvfp4_status nvfp4_int8_gemm(const int8_t* a_codes, const float* a_sc
     if (!status) return NVFP4_ERR_CUDA;
     const Operands o = {a_codes, w_codes, a_scale, w_scale, static_cast<uint16_t*>(y), ldy,
                         static_cast<int>(M), static_cast<int>(N), static_cast<int>(K)};
-    return M <= kFewMaxTokens ? launch_few(o, status, as_stream(stream))
+    return M <= kFewMaxTokens ? launch_few(o, info, status, as_stream(stream))
                               : launch_pair(o, info, status, as_stream(stream));
 }

@@ -39,4 +39,57 @@ __device__ __forceinline__ void tc_mma_i8_pair(uint32_t d_tmem, uint64_t adesc, 
         : "memory");
 }
 
+// Tries of mbar_spin before it gives up: at some 20 cycles a try at the least,
+// a bound of a fraction of a second to a few seconds.
+constexpr uint32_t kSpinTries = 1u << 25;
+
+// The feed loops' waits, by every lane of the warp.  mbar_peek tests a phase
+// without waiting; mbar_spin tests it until it has completed or `tries` tests
+// have failed (false then).  A loop peeks at its next stage before it issues
+// the work of the current one and spins only where that failed: a completed
+// phase costs some 60 cycles to test, and the tensor pipe runs dry meanwhile
+// when the test stands between two batches of MMAs (measured for batches of
+// four MMAs of 50-64 cycles: 366 cycles a batch with a wait in front of each,
+// 300 with the peek and the election hoisted, 206-256 with no wait at all).
+__device__ __forceinline__ bool mbar_peek(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+__device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity, uint32_t tries) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, %3;\n\t"
+        "SPIN:\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.gt.s32 q, n, 0;\n\t"
+        "@q bra SPIN;\n\t"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(tries)
+        : "memory");
+    return done != 0;
+}
+
+// 3-D tiled TMA load (no multicast), bytes counted on this CTA's `bar`.
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t x,
+                                            int32_t y, int32_t z, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(policy)
+        : "memory");
+}
+
 }  // namespace nvfp4

@@ -58,22 +58,26 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return l | (h << 16);
 }
 
-// Eight values of a row: r (the stored residual's value before rounding).
-template <bool kNorm>
-__device__ __forceinline__ void load_r(const RowArgs& a, int64_t row, int vec, float (&r)[8]) {
-    const uint4 xv = *reinterpret_cast<const uint4*>(a.x + row * a.ldx + 8 * static_cast<int64_t>(vec));
+// 16-byte load that does not allocate in L1.  An ordinary (coherent) load: the
+// residual may be rewritten in place by the thread that reads it.
+__device__ __forceinline__ uint4 ld_row16(const uint16_t* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// Eight values of r = x (+ residual), binary32.
+template <bool kRes>
+__device__ __forceinline__ void sum_r(const uint4& xv, const uint4& rv, float (&r)[8]) {
     const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+    const uint32_t rw[4] = {rv.x, rv.y, rv.z, rv.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         r[2 * i] = bf16_lo(xw[i]);
         r[2 * i + 1] = bf16_hi(xw[i]);
-    }
-    if (kNorm && a.residual) {
-        const uint4 rv =
-            *reinterpret_cast<const uint4*>(a.residual + row * a.ldr + 8 * static_cast<int64_t>(vec));
-        const uint32_t rw[4] = {rv.x, rv.y, rv.z, rv.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        if (kRes) {
             r[2 * i] = __fadd_rn(r[2 * i], bf16_lo(rw[i]));
             r[2 * i + 1] = __fadd_rn(r[2 * i + 1], bf16_hi(rw[i]));
         }
@@ -81,104 +85,202 @@ __device__ __forceinline__ void load_r(const RowArgs& a, int64_t row, int vec, f
 }
 
 template <bool kNorm>
-__device__ __forceinline__ void weigh(const RowArgs& a, int vec, const float (&r)[8], float (&t)[8]) {
-    if constexpr (kNorm) {
-        const uint4 wv = *reinterpret_cast<const uint4*>(a.weight + 8 * static_cast<int64_t>(vec));
-        const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+__device__ __forceinline__ void weigh(const uint4& wv, float offset, const float (&r)[8], float (&t)[8]) {
+    const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            t[2 * i] = __fmul_rn(r[2 * i], __fadd_rn(bf16_lo(ww[i]), a.weight_offset));
-            t[2 * i + 1] = __fmul_rn(r[2 * i + 1], __fadd_rn(bf16_hi(ww[i]), a.weight_offset));
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = r[i];
+    for (int i = 0; i < 4; ++i) {
+        t[2 * i] = kNorm ? __fmul_rn(r[2 * i], __fadd_rn(bf16_lo(ww[i]), offset)) : r[2 * i];
+        t[2 * i + 1] = kNorm ? __fmul_rn(r[2 * i + 1], __fadd_rn(bf16_hi(ww[i]), offset)) : r[2 * i + 1];
     }
 }
 
-// 8 codes from t and the multiplier fl32(127 / T).
-__device__ __forceinline__ uint2 encode8(const float (&t)[8], float mult) {
-    uint32_t b[2] = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        b[i >> 2] |= (static_cast<uint32_t>(__float2int_rn(__fmul_rn(t[i], mult))) & 0xFFu) << (8 * (i & 3));
-    return make_uint2(b[0], b[1]);
+__device__ __forceinline__ uint4 pack8(const float (&r)[8]) {
+    return make_uint4(pack_bf16(r[0], r[1]), pack_bf16(r[2], r[3]), pack_bf16(r[4], r[5]), pack_bf16(r[6], r[7]));
 }
 
-// One CTA per row at a time, two passes over it (the second from cache).
-constexpr int kRowThreads = 256;
+// 8 codes from t and the multiplier fl32(127 / T).  |t * mult| < 127.5, so
+// adding 1.5 * 2^23 rounds the product to an integer (ties to even) and leaves
+// its two's complement in the low byte: full-rate additions in place of
+// conversions, which run at a quarter of the rate.
+__device__ __forceinline__ uint2 encode8(const float (&t)[8], float mult) {
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(__fadd_rn(__fmul_rn(t[i], mult), 12582912.0f));
+    return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+                      __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+}
 
 template <bool kNorm>
-__global__ void __launch_bounds__(kRowThreads) row_int8_kernel(const RowArgs a) {
-    __shared__ float s_sum[2][kRowThreads / 32];
-    __shared__ uint32_t s_max[2][kRowThreads / 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ void tally(const float (&r)[8], const float (&t)[8], float& sum, uint32_t& top) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (kNorm) sum = __fmaf_rn(r[i], r[i], sum);
+        top = max(top, __float_as_uint(t[i]) & 0x7FFFFFFFu);    // NaN above infinity above all else
+    }
+}
+
+// Sum and maximum over the CTA's `warps` warps, the same in every thread: one
+// barrier, `red` alternating between two buffers from row to row.
+__device__ __forceinline__ void reduce_row(float& sum, uint32_t& top, uint2* red, int warps) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if (warps == 1) return;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) red[threadIdx.x >> 5] = make_uint2(__float_as_uint(sum), top);
+    __syncthreads();
+    const uint2 v = lane < warps ? red[lane] : make_uint2(0, 0);
+    sum = __uint_as_float(v.x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    top = __reduce_max_sync(0xFFFFFFFFu, v.y);
+}
+
+// The row's multiplier (bad rows: false) and, from one thread, its scale.
+template <bool kNorm>
+__device__ __forceinline__ bool finish_row(const RowArgs& a, int64_t row, float sum, uint32_t top, float* mult) {
+    const bool ok = top < 0x7F800000u && (!kNorm || sum < __uint_as_float(0x7F800000u));
+    const float T = fmaxf(__uint_as_float(top), kTiny);
+    *mult = __fdiv_rn(127.0f, T);
+    if (threadIdx.x == 0) {
+        float s = __fdiv_rn(T, 127.0f);
+        if (kNorm) s = __fmul_rn(s, __frsqrt_rn(__fmaf_rn(sum, a.inv_cols, a.eps)));
+        if (top == 0) s = 1.0f;
+        a.scale[row] = ok ? s : __uint_as_float(0x7FC00000u);
+    }
+    return ok;
+}
+
+// Rows that fit a CTA's registers: V vectors of 8 per thread, the vectors of a
+// thread blockDim.x apart.  Each CTA walks rows; the next row's loads leave
+// before the current row's reduction, and the norm's weights stay in registers.
+constexpr int row_max_threads(int v) { return v <= 2 ? 1024 : 640; }
+
+template <bool kNorm, bool kRes, int V>
+__global__ void __launch_bounds__(row_max_threads(V), 1) row_int8_kernel(const RowArgs a) {
+    __shared__ uint2 s_red[2][32];
+    grid_launch_dependents();
+    grid_dependency_wait();
     const int vecs = a.cols / 8;
+    const int warps = blockDim.x >> 5;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint4 w[V], xv[V], rv[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int v = threadIdx.x + j * blockDim.x;
+        const bool in = v < vecs;
+        w[j] = kNorm && in ? *reinterpret_cast<const uint4*>(a.weight + 8 * v) : zero;
+        xv[j] = in ? ld_row16(a.x + blockIdx.x * a.ldx + 8 * v) : zero;
+        rv[j] = kRes && in ? ld_row16(a.residual + blockIdx.x * a.ldr + 8 * v) : zero;
+    }
     int buf = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, buf ^= 1) {
+        float t[V][8];
         float sum = 0.0f;
         uint32_t top = 0;
-        for (int v = threadIdx.x; v < vecs; v += kRowThreads) {
-            float r[8], t[8];
-            load_r<kNorm>(a, row, v, r);
-            weigh<kNorm>(a, v, r, t);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (kNorm) sum = __fmaf_rn(r[i], r[i], sum);
-                top = max(top, __float_as_uint(t[i]) & 0x7FFFFFFFu);
+        for (int j = 0; j < V; ++j) {
+            float r[8];
+            sum_r<kRes>(xv[j], rv[j], r);
+            weigh<kNorm>(w[j], a.weight_offset, r, t[j]);
+            tally<kNorm>(r, t[j], sum, top);
+            const int v = threadIdx.x + j * blockDim.x;
+            if (kRes && v < vecs && a.residual_out)
+                *reinterpret_cast<uint4*>(a.residual_out + row * a.ldo + 8 * v) = pack8(r);
+        }
+        const int64_t next = row + gridDim.x;
+        if (next < a.rows) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int v = threadIdx.x + j * blockDim.x;
+                if (v < vecs) {
+                    xv[j] = ld_row16(a.x + next * a.ldx + 8 * v);
+                    if (kRes) rv[j] = ld_row16(a.residual + next * a.ldr + 8 * v);
+                }
             }
         }
+        reduce_row(sum, top, s_red[buf], warps);
+        float mult;
+        const bool ok = finish_row<kNorm>(a, row, sum, top, &mult);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        top = __reduce_max_sync(0xFFFFFFFFu, top);
-        if (lane == 0) {
-            s_sum[buf][warp] = sum;
-            s_max[buf][warp] = top;
-        }
-        __syncthreads();
-        sum = 0.0f;
-        top = 0;
-#pragma unroll
-        for (int w = 0; w < kRowThreads / 32; ++w) {
-            sum += s_sum[buf][w];
-            top = max(top, s_max[buf][w]);
-        }
-        const bool bad = top >= 0x7F800000u || (kNorm && !(sum < __uint_as_float(0x7F800000u)));
-        const float T = fmaxf(__uint_as_float(top), kTiny);
-        const float mult = bad ? 0.0f : __fdiv_rn(127.0f, T);
-        if (threadIdx.x == 0) {
-            float s = __fdiv_rn(T, 127.0f);
-            if (kNorm) s = __fmul_rn(s, __frsqrt_rn(__fmaf_rn(sum, a.inv_cols, a.eps)));
-            if (top == 0) s = 1.0f;
-            a.scale[row] = bad ? __uint_as_float(0x7FC00000u) : s;
-        }
-        for (int v = threadIdx.x; v < vecs; v += kRowThreads) {
-            float r[8], t[8];
-            load_r<kNorm>(a, row, v, r);
-            weigh<kNorm>(a, v, r, t);
-            if (kNorm && a.residual_out) {
-                uint4 o;
-                o.x = pack_bf16(r[0], r[1]);
-                o.y = pack_bf16(r[2], r[3]);
-                o.z = pack_bf16(r[4], r[5]);
-                o.w = pack_bf16(r[6], r[7]);
-                *reinterpret_cast<uint4*>(a.residual_out + row * a.ldo + 8 * static_cast<int64_t>(v)) = o;
-            }
-            const uint2 c = bad ? make_uint2(0, 0) : encode8(t, mult);
-            *reinterpret_cast<uint2*>(a.codes + row * a.cols + 8 * static_cast<int64_t>(v)) = c;
+        for (int j = 0; j < V; ++j) {
+            const int v = threadIdx.x + j * blockDim.x;
+            if (v < vecs)
+                *reinterpret_cast<uint2*>(a.codes + row * a.cols + 8 * v) =
+                    ok ? encode8(t[j], mult) : make_uint2(0, 0);
         }
     }
 }
 
-template <bool kNorm>
+// Longer rows: two passes, the second from cache.
+constexpr int kLongThreads = 512;
+
+template <bool kNorm, bool kRes>
+__global__ void __launch_bounds__(kLongThreads) row_int8_long_kernel(const RowArgs a) {
+    __shared__ uint2 s_red[2][32];
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int vecs = a.cols / 8;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    int buf = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, buf ^= 1) {
+        const uint16_t* x = a.x + row * a.ldx;
+        const uint16_t* res = kRes ? a.residual + row * a.ldr : nullptr;
+        float sum = 0.0f;
+        uint32_t top = 0;
+        for (int v = threadIdx.x; v < vecs; v += kLongThreads) {
+            const int64_t at = 8 * static_cast<int64_t>(v);
+            float r[8], t[8];
+            sum_r<kRes>(ld_row16(x + at), kRes ? ld_row16(res + at) : zero, r);
+            weigh<kNorm>(kNorm ? *reinterpret_cast<const uint4*>(a.weight + at) : zero, a.weight_offset, r, t);
+            tally<kNorm>(r, t, sum, top);
+        }
+        reduce_row(sum, top, s_red[buf], kLongThreads / 32);
+        float mult;
+        const bool ok = finish_row<kNorm>(a, row, sum, top, &mult);
+        for (int v = threadIdx.x; v < vecs; v += kLongThreads) {
+            const int64_t at = 8 * static_cast<int64_t>(v);
+            float r[8], t[8];
+            sum_r<kRes>(ld_row16(x + at), kRes ? ld_row16(res + at) : zero, r);
+            weigh<kNorm>(kNorm ? *reinterpret_cast<const uint4*>(a.weight + at) : zero, a.weight_offset, r, t);
+            if (kRes && a.residual_out) *reinterpret_cast<uint4*>(a.residual_out + row * a.ldo + at) = pack8(r);
+            *reinterpret_cast<uint2*>(a.codes + row * a.cols + at) = ok ? encode8(t, mult) : make_uint2(0, 0);
+        }
+    }
+}
+
+nvfp4_status launch(void (*kern)(RowArgs), int threads, const RowArgs& a, const DeviceInfo& dev, void* stream) {
+    // resident CTAs only: each walks its share of the rows
+    int per_sm = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0) != cudaSuccess || per_sm <= 0)
+        return NVFP4_ERR_CUDA;
+    const int64_t cap = static_cast<int64_t>(dev.sms) * per_sm;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.rows < cap ? a.rows : cap), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.stream = as_stream(stream);
+    // a programmatic dependent: the kernels wait for the previous grid before
+    // they touch global memory, so only their set-up overlaps it
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return NVFP4_ERR_CUDA;
+    return cuda_status(cudaGetLastError());
+}
+
+template <bool kNorm, bool kRes>
 nvfp4_status launch_rows(const RowArgs& a, void* stream) {
     DeviceInfo dev;
     const nvfp4_status st = require_sm100(&dev);
     if (st != NVFP4_OK) return st;
-    const int64_t cap = static_cast<int64_t>(dev.sms) * 8;
-    const int64_t grid = a.rows < cap ? a.rows : cap;
-    row_int8_kernel<kNorm><<<static_cast<unsigned>(grid), kRowThreads, 0, as_stream(stream)>>>(a);
-    return cuda_status(cudaGetLastError());
+    // the fewest vectors per thread whose threads fit a CTA
+    const int vecs = a.cols / 8;
+    auto threads = [&](int v) { return ((vecs + v - 1) / v + 31) / 32 * 32; };
+    if (threads(2) <= row_max_threads(2)) return launch(row_int8_kernel<kNorm, kRes, 2>, threads(2), a, dev, stream);
+    if (threads(4) <= row_max_threads(4)) return launch(row_int8_kernel<kNorm, kRes, 4>, threads(4), a, dev, stream);
+    return launch(row_int8_long_kernel<kNorm, kRes>, kLongThreads, a, dev, stream);
 }
 
 // Same address and stride: every element is read by the thread that rewrites
@@ -214,7 +316,7 @@ extern "C" nvfp4_status nvfp4_int8_quantize(const void* x, int64_t rows, int64_t
     a.cols = static_cast<int32_t>(cols);
     a.codes = reinterpret_cast<uint8_t*>(codes);
     a.scale = scale;
-    return launch_rows<false>(a, stream);
+    return launch_rows<false, false>(a, stream);
 }
 
 extern "C" nvfp4_status nvfp4_add_rms_norm_int8(const void* x, int64_t ldx, const void* residual,
@@ -272,5 +374,5 @@ extern "C" nvfp4_status nvfp4_add_rms_norm_int8(const void* x, int64_t ldx, cons
     a.cols = static_cast<int32_t>(cols);
     a.codes = reinterpret_cast<uint8_t*>(codes);
     a.scale = scale;
-    return launch_rows<true>(a, stream);
+    return residual ? launch_rows<true, true>(a, stream) : launch_rows<true, false>(a, stream);
 }
