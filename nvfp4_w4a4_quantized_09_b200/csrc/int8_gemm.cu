@@ -268,6 +268,7 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
     } else {
         // ---------------- epilogue (warps 2..9, both CTAs) ----------------
         grid_dependency_wait();
+        constexpr int kChunks = kPairMaxBN / 64;          // per warp
         const int q = warp & 3;
         const int half = (warp - 2) >> 2;
         const uint64_t pol_y = l2_policy_evict_first();
@@ -281,13 +282,21 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             pair_tile(t, args, mt, nt);
             const int m0 = mt * 256 + static_cast<int>(rank) * kRows + q * 32;   // row of lane 0
             const float sa = m0 + lane < args.M ? args.sa[m0 + lane] : 0.0f;
+            // the tile's channel scales are on their way while the MMAs run
+            float sw[kChunks];
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                const int c = half * 32 + 64 * i + lane;
+                sw[i] = m0 < args.M && c < BN && nt * BN + c < args.N ? args.sw[nt * BN + c] : 0.0f;
+            }
             if (!mbar_wait_warp(&tmem_full[acc], acc_phase, args.timeout_ns, s_abort, args.status)) break;
             tc_fence_after();
             if (m0 < args.M) {                                         // warp-uniform
-                for (int c = half * 32; c < BN; c += 64) {
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i) {
+                    const int c = half * 32 + 64 * i;
                     const int n0 = nt * BN + c;
-                    if (n0 >= args.N) break;                           // warp-uniform
-                    const float swl = n0 + lane < args.N ? args.sw[n0 + lane] : 0.0f;
+                    if (c >= BN || n0 >= args.N) break;                // warp-uniform
                     uint32_t r[32];
                     tmem_ld_32cols(tq + acc * 256 + c, r);
                     tmem_ld_wait();
@@ -295,9 +304,9 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const float v0 = scale_f32(static_cast<int32_t>(r[2 * j]), sa,
-                                                   __shfl_sync(0xFFFFFFFFu, swl, 2 * j));
+                                                   __shfl_sync(0xFFFFFFFFu, sw[i], 2 * j));
                         const float v1 = scale_f32(static_cast<int32_t>(r[2 * j + 1]), sa,
-                                                   __shfl_sync(0xFFFFFFFFu, swl, 2 * j + 1));
+                                                   __shfl_sync(0xFFFFFFFFu, sw[i], 2 * j + 1));
                         o[j] = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(v0))) |
                                (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(v1))) << 16);
                     }
@@ -440,13 +449,18 @@ void launch_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2], int 
 }
 
 nvfp4_status launch_few(const Operands& o, const DeviceInfo& info, int* status, cudaStream_t stream) {
-    auto kern = int8_gemm_few_kernel;
+    using Kernel = void (*)(CUtensorMap, CUtensorMap, FewArgs);
+    static const Kernel kernels[4] = {int8_gemm_few_kernel<1>, int8_gemm_few_kernel<2>, int8_gemm_few_kernel<4>,
+                                      int8_gemm_few_kernel<8>};
     static PerDeviceOnce once;
     int dev = 0;
     nvfp4_status st = current_device(&dev);
     if (st != NVFP4_OK) return st;
     st = once.run(dev, [&] {
-        return cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem));
+        for (const Kernel k : kernels)
+            if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem) != cudaSuccess)
+                return NVFP4_ERR_CUDA;
+        return NVFP4_OK;
     });
     if (st != NVFP4_OK) return st;
     FewArgs f = {};
@@ -455,23 +469,30 @@ nvfp4_status launch_few(const Operands& o, const DeviceInfo& info, int* status, 
     f.k_steps = (o.K + kStepBytes - 1) / kStepBytes;
     f.timeout_ns = kTimeoutNs;
     f.status = status;
-    // Tile width: a k-step costs the largest of its MMA time (2 BN cycles), its
-    // feed (128 bytes a row at about 70 bytes per cycle and SM) and the SMs'
-    // common share of memory (about 3400 bytes per cycle); take the width whose
-    // rounds of tiles cost least, the narrowest among equals.
+    // Tile width.  Over all rounds of tiles an SM spends on each k-step the
+    // larger of its MMAs (four of BN / 2 cycles, 52 at the least, and 230 for a
+    // stage's handshake) and its feed (about 42 bytes a cycle while all SMs
+    // stream); memory as a whole delivers some 3400 bytes of weights a cycle.
+    // The slower of the two decides; a quarter of the SMs' share is added, so
+    // that among widths that memory bounds the least loaded SMs win, and the
+    // narrowest among equals.
+    int u = 0;
     int64_t best = 0;
+    const int64_t memory = o.N * static_cast<int64_t>(kStepBytes) / 3400;
     for (int bn = 16; bn <= kFewMaxBN; bn += 16) {
         const int64_t tiles = (o.N + bn - 1) / bn;
-        const int64_t rounds = (tiles + info.sms - 1) / info.sms;
-        const int64_t step = std::max<int64_t>(std::max(2 * bn, (f.nt + bn) * kStepBytes / 70),
-                                               std::min<int64_t>(tiles, info.sms) * bn * kStepBytes / 3400);
-        if (best == 0 || rounds * step < best) best = rounds * step, f.bn = bn;
+        int bu = 0, bs = 0;
+        few_config(f.nt, bn, &bu, &bs);
+        const int64_t sm = (tiles + info.sms - 1) / info.sms *
+                           std::max(4 * std::max(52, bn / 2) + 230 / bu, (f.nt + bn) * kStepBytes / 42);
+        const int64_t cost = 4 * std::max(sm, memory) + sm;
+        if (best == 0 || cost < best) best = cost, f.bn = bn, f.stages = bs, u = bu;
     }
     f.n_tiles = (o.N + f.bn - 1) / f.bn;
-    few_config(f.nt, f.bn, &f.u, &f.stages);
+    const Kernel kern = kernels[u == 8 ? 3 : u / 2];
     CUtensorMap ta, tw;
     f.wide = o.K % kStepBytes == 0;
-    if (!make_steps_map(&ta, o.a, o.M, o.K, f.nt, f.u) || !make_steps_map(&tw, o.w, o.N, o.K, f.bn, f.u))
+    if (!make_steps_map(&ta, o.a, o.M, o.K, f.nt, u) || !make_steps_map(&tw, o.w, o.N, o.K, f.bn, u))
         return NVFP4_ERR_CUDA;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];

@@ -8,10 +8,9 @@
 //     reads 128 rows from the tile's start; the rows beyond NT are whatever
 //     shared memory holds there, and the accumulator lanes they fill are never
 //     read.
-//   * A pipeline stage holds U steps of 128 values of K, U chosen so that a
-//     stage is some 24 KB: each stage costs the producer and the MMA warp one
-//     handshake, whose latency would otherwise exceed the stream's time when
-//     BN is small.
+//   * A pipeline stage holds U = 1, 2, 4 or 8 steps of 128 values of K, the
+//     most that 58 KB take: each stage costs the MMA warp a handshake during
+//     which the tensor pipe idles, and each operand one copy.
 //   * Persistent: the ring runs across tiles, two accumulators of 256 columns.
 //   * Launched as a programmatic dependent: every role that touches global
 //     memory first waits for the previous grid (griddepcontrol.wait).
@@ -23,7 +22,6 @@
 constexpr int kFewThreads = 320;
 constexpr int kFewMaxTokens = 128;
 constexpr int kFewMaxStages = 16;
-constexpr int kFewMaxU = 8;
 constexpr int kFewMaxBN = 256;
 constexpr uint32_t kFewSmem = 227 * 1024;            // whole: one CTA per SM
 constexpr uint32_t kFewBars = (2 * kFewMaxStages + 5) * 8;
@@ -38,7 +36,6 @@ struct FewArgs {
     int n_tiles, k_steps;
     int nt;          // token rows loaded: M rounded up to 8
     int bn;          // channels per tile
-    int u;           // k-steps per stage
     int wide;        // one copy brings a stage's U steps of an operand
     int stages;
     uint64_t timeout_ns;
@@ -48,21 +45,21 @@ struct FewArgs {
 // k-steps per stage and ring depth of a tile shape.
 __host__ __device__ constexpr void few_config(int nt, int bn, int* u, int* stages) {
     const int step = (nt + bn) * kStepBytes;
-    int uu = 24 * 1024 / step;
-    uu = uu < 1 ? 1 : uu > kFewMaxU ? kFewMaxU : uu;
+    int uu = 58 * 1024 / step;
+    uu = uu >= 8 ? 8 : uu >= 4 ? 4 : uu >= 2 ? 2 : 1;
     int st = static_cast<int>(kFewRing) / (uu * step);
     *u = uu;
     *stages = st > kFewMaxStages ? kFewMaxStages : st;
 }
 
-// Every shape keeps at least four stages, and the MMA's 128 rows from the last
+// Every shape keeps at least three stages, and the MMA's 128 rows from the last
 // A tile's start end inside the ring (the B tiles follow the A tiles).
 constexpr bool few_configs_fit() {
     for (int nt = 8; nt <= kFewMaxTokens; nt += 8)
         for (int bn = 16; bn <= kFewMaxBN; bn += 16) {
             int u = 0, st = 0;
             few_config(nt, bn, &u, &st);
-            if (st < 4 || static_cast<uint32_t>(st * u * (nt + bn) * kStepBytes) > kFewRing) return false;
+            if (st < 3 || static_cast<uint32_t>(st * u * (nt + bn) * kStepBytes) > kFewRing) return false;
             if (st * u * bn < kRows - nt) return false;
         }
     return true;
@@ -70,13 +67,14 @@ constexpr bool few_configs_fit() {
 static_assert(few_configs_fit(), "a few-token configuration does not fit");
 static_assert(kFewSmem > 228 * 1024 / 2, "two CTAs could share an SM and its 512 TMEM columns");
 
+template <int U>
 __global__ void __launch_bounds__(kFewThreads, 1)
 int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
                      const __grid_constant__ CUtensorMap tmap_w, const FewArgs args) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const int STAGES = args.stages, U = args.u, BN = args.bn;
+    const int STAGES = args.stages, BN = args.bn;
     const uint32_t a_step = static_cast<uint32_t>(args.nt) * kStepBytes;
     const uint32_t b_step = static_cast<uint32_t>(BN) * kStepBytes;
     const uint32_t off_b = static_cast<uint32_t>(STAGES * U) * a_step;
@@ -129,6 +127,13 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
     const bool leader = elect_one();
     if (warp == 0) {
         // ---------------- TMA producer ----------------
+        // While the previous grid finishes, the first ring of weights moves
+        // into L2 (a hint: nothing of it is read before the wait).
+        if (leader && args.wide) {
+            const int ahead = min(STAGES, k_stages);
+            for (int ks = 0; ks < ahead; ++ks)
+                tma_prefetch_3d(&tmap_w, 0, static_cast<int>(blockIdx.x) * BN, ks * U);
+        }
         grid_dependency_wait();
         const uint64_t pol_w = l2_policy_evict_first();   // each weight byte is read once
         const uint64_t pol_a = l2_policy_evict_last();    // tokens are read by every tile
@@ -188,7 +193,7 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
         const uint32_t idesc = int8_idesc(kRows, BN);
         const uint64_t da0 = sdesc_kmajor_sw128(smem_u32(smem));
         const uint64_t db0 = sdesc_kmajor_sw128(smem_u32(smem + off_b));
-        const int last_n = (args.K - (args.k_steps - 1) * kStepBytes + 31) / 32;   // MMAs of the last step
+        const int last_n = (args.K - (k_stages - 1) * U * kStepBytes + 31) / 32;   // MMAs of the last stage
         const uint32_t acc_empty0 = smem_u32(tmem_empty);
         bool failed = false;
         int stage = 0, acc = 0;
@@ -204,19 +209,24 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 const int next = stage + 1 == STAGES ? 0 : stage + 1;
                 const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
                 ready = mbar_peek(full0 + 8 * next, next_phase);
-                const int k0 = ks * U;
-                const int steps = min(U, args.k_steps - k0);
+                // descriptor start addresses advance by 2 per 32 bytes of K
+                const uint64_t da = da0 + static_cast<uint64_t>(stage * U) * (a_step >> 4);
+                const uint64_t db = db0 + static_cast<uint64_t>(stage * U) * (b_step >> 4);
                 if (leader && !failed) {
-                    for (int i = 0; i < steps; ++i) {
-                        // descriptor start addresses advance by 2 per 32 bytes of K
-                        const uint64_t da = da0 + ((stage * U + i) * a_step >> 4);
-                        const uint64_t db = db0 + ((stage * U + i) * b_step >> 4);
-                        const int nmma = k0 + i == args.k_steps - 1 ? last_n : kStepBytes / 32;
+                    if (ks + 1 < k_stages) {
 #pragma unroll
-                        for (int j = 0; j < kStepBytes / 32; ++j)
-                            if (j < nmma)
-                                tc_mma_i8(d_tmem, da + 2 * j, db + 2 * j, idesc,
-                                          static_cast<uint32_t>((k0 + i) | j));
+                        for (int i = 0; i < U; ++i)
+#pragma unroll
+                            for (int j = 0; j < kStepBytes / 32; ++j)
+                                tc_mma_i8(d_tmem, da + i * (a_step >> 4) + 2 * j, db + i * (b_step >> 4) + 2 * j,
+                                          idesc, static_cast<uint32_t>(ks | i | j));
+                    } else {
+                        // the last stage ends with K
+                        for (int i = 0; i < last_n; ++i) {
+                            const uint32_t j = 2 * (i & 3);
+                            tc_mma_i8(d_tmem, da + (i >> 2) * (a_step >> 4) + j, db + (i >> 2) * (b_step >> 4) + j,
+                                      idesc, static_cast<uint32_t>(ks | i));
+                        }
                     }
                     tc_commit(&empty[stage]);
                     if (ks == k_stages - 1) tc_commit(&tmem_full[acc]);
@@ -245,6 +255,7 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
         // lane -> token; 16 channels at a time, a 32-byte sector of the row
         const int q = warp & 3;                       // TMEM lane quarter of this warp
         const int half = (warp - 2) >> 2;
+        constexpr int kChunks = kFewMaxBN / 32;       // per warp
         const int m0 = q * 32;
         const uint32_t tq = tmem_base + (static_cast<uint32_t>(m0) << 16);
         grid_dependency_wait();
@@ -253,13 +264,21 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int nt = blockIdx.x; nt < args.n_tiles; nt += gridDim.x) {
+            // the tile's channel scales are on their way while the MMAs run
+            float sw[kChunks];
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                const int c = half * 16 + 32 * i + (lane & 15);
+                sw[i] = m0 < args.M && c < BN && nt * BN + c < args.N ? args.sw[nt * BN + c] : 0.0f;
+            }
             if (!mbar_wait_warp(&tmem_full[acc], acc_phase, args.timeout_ns, s_abort, args.status)) break;
             tc_fence_after();
             if (m0 < args.M) {                                         // warp-uniform
-                for (int c = half * 16; c < BN; c += 32) {
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i) {
+                    const int c = half * 16 + 32 * i;
                     const int n0 = nt * BN + c;
-                    if (n0 >= args.N) break;                           // warp-uniform
-                    const float swl = lane < 16 && n0 + lane < args.N ? args.sw[n0 + lane] : 0.0f;
+                    if (c >= BN || n0 >= args.N) break;                // warp-uniform
                     uint32_t r[16];
                     tmem_ld_16cols(tq + acc * 256 + c, r);
                     tmem_ld_wait();
@@ -267,9 +286,9 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const uint32_t lo = scale_bf16(static_cast<int32_t>(r[2 * j]), sa,
-                                                       __shfl_sync(0xFFFFFFFFu, swl, 2 * j));
+                                                       __shfl_sync(0xFFFFFFFFu, sw[i], 2 * j));
                         const uint32_t hi = scale_bf16(static_cast<int32_t>(r[2 * j + 1]), sa,
-                                                       __shfl_sync(0xFFFFFFFFu, swl, 2 * j + 1));
+                                                       __shfl_sync(0xFFFFFFFFu, sw[i], 2 * j + 1));
                         o[j] = lo | (hi << 16);
                     }
                     if (m0 + lane < args.M) {
