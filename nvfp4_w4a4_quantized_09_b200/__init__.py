@@ -599,11 +599,6 @@ class Int8Tensor:
         return cls(torch.cat([t.codes for t in tensors]), torch.cat([t.scale for t in tensors]))
 
 
-def _ld(t: torch.Tensor) -> int:
-    """Row stride in elements; a single row has none of its own."""
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
-
-
 def _empty(*shape, dtype, device, stream):
     """torch.empty for a kernel on `stream`: with an explicit stream the memory
     is that stream's, so that no earlier use of it on another one can still be
@@ -617,22 +612,8 @@ def _empty(*shape, dtype, device, stream):
     return t
 
 
-# The calls below take a few microseconds on the device for a decode step, so
-# the checks of a correct call are kept to plain attribute reads: the device by
-# its index, the stream by its handle.
-def _on_current_device(names, tensors) -> torch.device:
-    index = tensors[0].get_device()
-    same = index >= 0 and index == torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != index:
-            same = False
-    if not same:
-        _check_devices(**dict(zip(names, tensors)))          # raises, naming the tensor
-    return tensors[0].device
-
-
-def _stream_handle(device: torch.device, stream) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+def _stream_handle(index: int, stream) -> int:
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _check_codes(t, name: str, shape=None):
@@ -648,23 +629,34 @@ def _check_row_scale(t, name: str, rows: int):
         raise ValueError(f"{name} must be a contiguous float32 tensor of {rows} elements")
 
 
+# The three calls below take a few microseconds on the device for a decode
+# step, so the device check of a correct call reads device indices only (an
+# outsider sends it to _check_devices, which names the tensor), the stream is
+# taken by its handle, and a single row's stride, which torch may report as
+# anything, is given as the row's length rounded up to 8.
 def int8_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
                   scale: Optional[torch.Tensor] = None, stream=None):
     """int8 codes [rows, cols] and FP32 scales [rows] of a BF16 matrix:
     codes = RNE(x * (127 / max|row|)), scale = max|row| / 127."""
     _check_bf16_matrix(x, "x")
     rows, cols = x.shape
+    dev = x.get_device()
+    same = dev >= 0 and dev == torch.cuda.current_device()
     if codes is not None:
         _check_codes(codes, "codes", x.shape)
+        same = same and codes.get_device() == dev
     if scale is not None:
         _check_row_scale(scale, "scale", rows)
-    dev = _on_current_device(("x", "codes", "scale"), (x, codes, scale))
+        same = same and scale.get_device() == dev
+    if not same:
+        _check_devices(x=x, codes=codes, scale=scale)
     if codes is None:
-        codes = _empty(rows, cols, dtype=torch.int8, device=dev, stream=stream)
+        codes = _empty(rows, cols, dtype=torch.int8, device=x.device, stream=stream)
     if scale is None:
-        scale = _empty(rows, dtype=torch.float32, device=dev, stream=stream)
-    st = _lib.lib().nvfp4_int8_quantize(x.data_ptr(), rows, cols, _ld(x), codes.data_ptr(),
-                                        scale.data_ptr(), _stream_handle(dev, stream))
+        scale = _empty(rows, dtype=torch.float32, device=x.device, stream=stream)
+    st = _lib.lib().nvfp4_int8_quantize(
+        x.data_ptr(), rows, cols, x.stride(0) if rows > 1 else (cols + 7) // 8 * 8, codes.data_ptr(),
+        scale.data_ptr(), _stream_handle(dev, stream))
     if st:
         raise Nvfp4Error("nvfp4_int8_quantize", st)
     return codes, scale
@@ -690,32 +682,42 @@ def add_rms_norm_int8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[
     if not isinstance(weight, torch.Tensor) or weight.dtype != torch.bfloat16 \
             or weight.shape != (cols,) or not weight.is_contiguous():
         raise ValueError(f"weight must be a contiguous bfloat16 tensor of {cols} elements")
+    dev = x.get_device()
+    same = dev >= 0 and dev == torch.cuda.current_device() and weight.get_device() == dev
     if residual is not None:
         _check_bf16_matrix(residual, "residual")
         if residual.shape != x.shape:
             raise ValueError(f"residual must have shape {tuple(x.shape)}, got {tuple(residual.shape)}")
+        same = same and residual.get_device() == dev
         if residual_out is not None:
             _check_out_matrix(residual_out, "residual_out", torch.bfloat16, rows, cols)
+            same = same and residual_out.get_device() == dev
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     if codes is not None:
         _check_codes(codes, "codes", x.shape)
+        same = same and codes.get_device() == dev
     if scale is not None:
         _check_row_scale(scale, "scale", rows)
-    dev = _on_current_device(("x", "weight", "residual", "residual_out", "codes", "scale"),
-                             (x, weight, residual, residual_out, codes, scale))
+        same = same and scale.get_device() == dev
+    if not same:
+        _check_devices(x=x, weight=weight, residual=residual, residual_out=residual_out, codes=codes,
+                       scale=scale)
+    device = x.device
     if codes is None:
-        codes = _empty(rows, cols, dtype=torch.int8, device=dev, stream=stream)
+        codes = _empty(rows, cols, dtype=torch.int8, device=device, stream=stream)
     if scale is None:
-        scale = _empty(rows, dtype=torch.float32, device=dev, stream=stream)
+        scale = _empty(rows, dtype=torch.float32, device=device, stream=stream)
+    one = (cols + 7) // 8 * 8 if rows <= 1 else 0
     r = ldr = out = ldo = 0
     if residual is not None:
         if residual_out is None:
-            residual_out = _empty(rows, cols, dtype=torch.bfloat16, device=dev, stream=stream)
-        r, ldr, out, ldo = residual.data_ptr(), _ld(residual), residual_out.data_ptr(), _ld(residual_out)
+            residual_out = _empty(rows, cols, dtype=torch.bfloat16, device=device, stream=stream)
+        r, ldr = residual.data_ptr(), one or residual.stride(0)
+        out, ldo = residual_out.data_ptr(), one or residual_out.stride(0)
     st = _lib.lib().nvfp4_add_rms_norm_int8(
-        x.data_ptr(), _ld(x), r, ldr, weight.data_ptr(), weight_offset, eps, rows, cols, out, ldo,
-        codes.data_ptr(), scale.data_ptr(), _stream_handle(dev, stream))
+        x.data_ptr(), one or x.stride(0), r, ldr, weight.data_ptr(), weight_offset, eps, rows, cols,
+        out, ldo, codes.data_ptr(), scale.data_ptr(), _stream_handle(dev, stream))
     if st:
         raise Nvfp4Error("nvfp4_add_rms_norm_int8", st)
     return Int8Tensor(codes, scale), residual_out
@@ -730,20 +732,28 @@ def int8_gemm(a: Int8Tensor, w: Int8Tensor, y: Optional[torch.Tensor] = None,
     _check_codes(ac, "a.codes")
     _check_codes(wc, "w.codes")
     M, K = ac.shape
-    N = wc.shape[0]
-    if wc.shape[1] != K:
+    N, Kw = wc.shape
+    if Kw != K:
         raise ValueError("inner dimensions differ")
     _check_row_scale(asc, "a.scale", M)
     _check_row_scale(wsc, "w.scale", N)
+    dev = ac.get_device()
+    same = dev >= 0 and dev == torch.cuda.current_device() and \
+        asc.get_device() == wc.get_device() == wsc.get_device() == dev
     if y is not None:
         _check_out_matrix(y, "y", torch.bfloat16, M, N)
-    dev = _on_current_device(("a_codes", "a_scale", "w_codes", "w_scale", "y"), (ac, asc, wc, wsc, y))
+        same = same and y.get_device() == dev
+    if not same:
+        _check_devices(a_codes=ac, a_scale=asc, w_codes=wc, w_scale=wsc, y=y)
+    ldy = (N + 7) // 8 * 8
     if y is None:
-        y = _empty(M, (N + 7) // 8 * 8, dtype=torch.bfloat16, device=dev, stream=stream)
-        if N % 8:
+        y = _empty(M, ldy, dtype=torch.bfloat16, device=ac.device, stream=stream)
+        if ldy != N:
             y = y[:, :N]
+    elif M > 1:
+        ldy = y.stride(0)
     st = _lib.lib().nvfp4_int8_gemm(ac.data_ptr(), asc.data_ptr(), wc.data_ptr(), wsc.data_ptr(),
-                                    y.data_ptr(), _ld(y), M, N, K, _stream_handle(dev, stream))
+                                    y.data_ptr(), ldy, M, N, K, _stream_handle(dev, stream))
     if st:
         raise Nvfp4Error("nvfp4_int8_gemm", st)
     return y

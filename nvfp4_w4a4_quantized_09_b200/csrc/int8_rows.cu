@@ -23,6 +23,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "host_common.h"
 #include "nvfp4.h"
 #include "ptx.cuh"
@@ -249,11 +251,26 @@ __global__ void __launch_bounds__(kLongThreads) row_int8_long_kernel(const RowAr
     }
 }
 
-nvfp4_status launch(void (*kern)(RowArgs), int threads, const RowArgs& a, const DeviceInfo& dev, void* stream) {
+// `resident`: CTAs of `kern` per SM for each thread count in warps, 0 until
+// measured (racing threads measure the same value).
+struct Resident {
+    std::atomic<int> per_sm[kMaxDevices][33] = {};
+};
+
+nvfp4_status launch(void (*kern)(RowArgs), Resident& resident, int threads, const RowArgs& a, void* stream) {
+    DeviceInfo dev;
+    int id = 0;
+    nvfp4_status st = require_sm100(&dev);
+    if (st == NVFP4_OK) st = current_device(&id);
+    if (st != NVFP4_OK) return st;
     // resident CTAs only: each walks its share of the rows
-    int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0) != cudaSuccess || per_sm <= 0)
-        return NVFP4_ERR_CUDA;
+    std::atomic<int>& cached = resident.per_sm[id][threads / 32];
+    int per_sm = cached.load(std::memory_order_relaxed);
+    if (per_sm <= 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0) != cudaSuccess || per_sm <= 0)
+            return NVFP4_ERR_CUDA;
+        cached.store(per_sm, std::memory_order_relaxed);
+    }
     const int64_t cap = static_cast<int64_t>(dev.sms) * per_sm;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows < cap ? a.rows : cap), 1, 1);
@@ -272,15 +289,13 @@ nvfp4_status launch(void (*kern)(RowArgs), int threads, const RowArgs& a, const 
 
 template <bool kNorm, bool kRes>
 nvfp4_status launch_rows(const RowArgs& a, void* stream) {
-    DeviceInfo dev;
-    const nvfp4_status st = require_sm100(&dev);
-    if (st != NVFP4_OK) return st;
+    static Resident r2, r4, rl;
     // the fewest vectors per thread whose threads fit a CTA
     const int vecs = a.cols / 8;
     auto threads = [&](int v) { return ((vecs + v - 1) / v + 31) / 32 * 32; };
-    if (threads(2) <= row_max_threads(2)) return launch(row_int8_kernel<kNorm, kRes, 2>, threads(2), a, dev, stream);
-    if (threads(4) <= row_max_threads(4)) return launch(row_int8_kernel<kNorm, kRes, 4>, threads(4), a, dev, stream);
-    return launch(row_int8_long_kernel<kNorm, kRes>, kLongThreads, a, dev, stream);
+    if (threads(2) <= row_max_threads(2)) return launch(row_int8_kernel<kNorm, kRes, 2>, r2, threads(2), a, stream);
+    if (threads(4) <= row_max_threads(4)) return launch(row_int8_kernel<kNorm, kRes, 4>, r4, threads(4), a, stream);
+    return launch(row_int8_long_kernel<kNorm, kRes>, rl, kLongThreads, a, stream);
 }
 
 // Same address and stride: every element is read by the thread that rewrites
