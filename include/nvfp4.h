@@ -381,8 +381,8 @@ nvfp4_status nvfp4_int8_quantize(const void* x, int64_t rows, int64_t cols, int6
  * (the factor rstd is common to the row, so the codes do not depend on it).
  * residual_out receives r rounded once to BF16; the norm reads r unrounded.
  * A row whose t is zero throughout has scale 1.  A row with a NaN or an
- * infinity in x, residual, r or t, or whose sum of squares exceeds binary32,
- * gets scale NaN and codes 0 (residual_out holds r all the same).
+ * infinity in x, residual, weight, r or t, or whose sum of squares exceeds
+ * binary32, gets scale NaN and codes 0 (residual_out holds r all the same).
  *   x, residual, residual_out (device) BF16 [rows, cols], row strides ldx, ldr,
  *     ldo elements; residual may be NULL (ldr unused); residual_out may be
  *     NULL (ldo unused) and must be NULL without a residual.  residual_out may
@@ -390,7 +390,7 @@ nvfp4_status nvfp4_int8_quantize(const void* x, int64_t rows, int64_t cols, int6
  *     written in place.  Any other overlap of an output with an input or
  *     another output is refused.
  *   weight (device) BF16 [cols]; weight_offset 0, or 1 for weights stored as
- *     their difference from one (any finite value below 2^127 is accepted).
+ *     their difference from one (any value of magnitude below 2^100 is accepted).
  *   eps in [2^-126, 2^127).
  *   codes (device, rows * cols bytes), scale (device, rows FP32).
  * Requirements: cols % 16 == 0, cols >= 16, strides % 8 == 0 and >= cols;

@@ -213,6 +213,9 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
     } else if (warp == 1) {
         if (rank == 0) {
             // ---------------- MMA issuer (even CTA) ----------------
+            // nothing here reads memory; the bounded waits below begin when the
+            // previous grid, however long it takes, has finished
+            grid_dependency_wait();
             const uint32_t idesc = int8_idesc(256, BN);
             const uint64_t da0 = sdesc_kmajor_sw128(smem_u32(smem));
             const uint64_t db0 = sdesc_kmajor_sw128(smem_u32(smem + off_b));

@@ -190,6 +190,9 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
         __syncwarp();
     } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
+        // nothing here reads memory; the bounded waits below begin when the
+        // previous grid, however long it takes, has finished
+        grid_dependency_wait();
         const uint32_t idesc = int8_idesc(kRows, BN);
         const uint64_t da0 = sdesc_kmajor_sw128(smem_u32(smem));
         const uint64_t db0 = sdesc_kmajor_sw128(smem_u32(smem + off_b));

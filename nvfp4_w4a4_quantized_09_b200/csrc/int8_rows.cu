@@ -121,20 +121,34 @@ __device__ __forceinline__ void tally(const float (&r)[8], const float (&t)[8], 
     }
 }
 
+// No norm: BF16 magnitudes compared as 16-bit integers, two at a time.
+__device__ __forceinline__ uint32_t tally16(const uint4& xv, uint32_t top2) {
+    top2 = __vmaxu2(top2, xv.x & 0x7FFF7FFFu);
+    top2 = __vmaxu2(top2, xv.y & 0x7FFF7FFFu);
+    top2 = __vmaxu2(top2, xv.z & 0x7FFF7FFFu);
+    return __vmaxu2(top2, xv.w & 0x7FFF7FFFu);
+}
+__device__ __forceinline__ uint32_t top_bits(uint32_t top2) { return max(top2 & 0xFFFFu, top2 >> 16) << 16; }
+
 // Sum and maximum over the CTA's `warps` warps, the same in every thread: one
 // barrier, `red` alternating between two buffers from row to row.
+template <bool kNorm>
 __device__ __forceinline__ void reduce_row(float& sum, uint32_t& top, uint2* red, int warps) {
+    if (kNorm) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    }
     top = __reduce_max_sync(0xFFFFFFFFu, top);
     if (warps == 1) return;
     const int lane = threadIdx.x & 31;
     if (lane == 0) red[threadIdx.x >> 5] = make_uint2(__float_as_uint(sum), top);
     __syncthreads();
     const uint2 v = lane < warps ? red[lane] : make_uint2(0, 0);
-    sum = __uint_as_float(v.x);
+    if (kNorm) {
+        sum = __uint_as_float(v.x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    }
     top = __reduce_max_sync(0xFFFFFFFFu, v.y);
 }
 
@@ -154,12 +168,16 @@ __device__ __forceinline__ bool finish_row(const RowArgs& a, int64_t row, float 
 }
 
 // Rows that fit a CTA's registers: V vectors of 8 per thread, the vectors of a
-// thread blockDim.x apart.  Each CTA walks rows; the next row's loads leave
-// before the current row's reduction, and the norm's weights stay in registers.
-constexpr int row_max_threads(int v) { return v <= 2 ? 1024 : 640; }
+// thread blockDim.x apart.  Each CTA walks rows, and the next row's loads leave
+// before the current row's reduction.  Between that and the encoding the norm
+// holds t (with its weights in registers); without a norm the row is held as
+// loaded.  What counts is bytes in flight: thread counts and register limits
+// are set so that two CTAs or more share an SM where that is possible.
+constexpr int row_max_threads(bool norm, int v) { return v == 2 ? (norm ? 1024 : 768) : 640; }
+constexpr int row_min_ctas(bool norm, int v) { return norm || v == 8 ? 1 : 2; }
 
 template <bool kNorm, bool kRes, int V>
-__global__ void __launch_bounds__(row_max_threads(V), 1) row_int8_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(row_max_threads(kNorm, V), row_min_ctas(kNorm, V)) row_int8_kernel(const RowArgs a) {
     __shared__ uint2 s_red[2][32];
     grid_launch_dependents();
     grid_dependency_wait();
@@ -177,18 +195,24 @@ __global__ void __launch_bounds__(row_max_threads(V), 1) row_int8_kernel(const R
     }
     int buf = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, buf ^= 1) {
-        float t[V][8];
+        float t[kNorm ? V : 1][8];
+        uint4 held[kNorm ? 1 : V];
         float sum = 0.0f;
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            float r[8];
-            sum_r<kRes>(xv[j], rv[j], r);
-            weigh<kNorm>(w[j], a.weight_offset, r, t[j]);
-            tally<kNorm>(r, t[j], sum, top);
-            const int v = threadIdx.x + j * blockDim.x;
-            if (kRes && v < vecs && a.residual_out)
-                *reinterpret_cast<uint4*>(a.residual_out + row * a.ldo + 8 * v) = pack8(r);
+            if constexpr (kNorm) {
+                float r[8];
+                sum_r<kRes>(xv[j], rv[j], r);
+                weigh<kNorm>(w[j], a.weight_offset, r, t[j]);
+                tally<kNorm>(r, t[j], sum, top);
+                const int v = threadIdx.x + j * blockDim.x;
+                if (kRes && v < vecs && a.residual_out)
+                    *reinterpret_cast<uint4*>(a.residual_out + row * a.ldo + 8 * v) = pack8(r);
+            } else {
+                held[j] = xv[j];
+                top = tally16(xv[j], top);
+            }
         }
         const int64_t next = row + gridDim.x;
         if (next < a.rows) {
@@ -201,26 +225,42 @@ __global__ void __launch_bounds__(row_max_threads(V), 1) row_int8_kernel(const R
                 }
             }
         }
-        reduce_row(sum, top, s_red[buf], warps);
+        if constexpr (!kNorm) top = top_bits(top);
+        reduce_row<kNorm>(sum, top, s_red[buf], warps);
         float mult;
         const bool ok = finish_row<kNorm>(a, row, sum, top, &mult);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int v = threadIdx.x + j * blockDim.x;
-            if (v < vecs)
-                *reinterpret_cast<uint2*>(a.codes + row * a.cols + 8 * v) =
-                    ok ? encode8(t[j], mult) : make_uint2(0, 0);
+            if (v < vecs) {
+                uint2 c = make_uint2(0, 0);
+                if constexpr (kNorm) {
+                    if (ok) c = encode8(t[j], mult);
+                } else {
+                    float x8[8];
+                    sum_r<false>(held[j], zero, x8);
+                    if (ok) c = encode8(x8, mult);
+                }
+                *reinterpret_cast<uint2*>(a.codes + row * a.cols + 8 * v) = c;
+            }
         }
     }
 }
 
-// Longer rows: two passes, the second from cache.
+// Longer rows: t waits in shared memory (as x itself, in 16 bits, without a
+// norm) between the reduction and the encoding.  Each thread reads back what it
+// wrote; several CTAs per SM keep loads in flight.
 constexpr int kLongThreads = 512;
+constexpr int kLongBatch = 4;
+constexpr int kLongSmem = 200 * 1024;
 
-template <bool kNorm, bool kRes>
-__global__ void __launch_bounds__(kLongThreads) row_int8_long_kernel(const RowArgs a) {
+template <bool kNorm, bool kRes, bool kStaged>
+__global__ void __launch_bounds__(kLongThreads, 2) row_int8_long_kernel(const RowArgs a) {
     __shared__ uint2 s_red[2][32];
-    grid_launch_dependents();
+    extern __shared__ uint4 s_row[];
+    // rows of any length: the next grid is let in early only where this one is
+    // short beside the bounded waits of the kernels that may follow
+    if (kStaged) grid_launch_dependents();
     grid_dependency_wait();
     const int vecs = a.cols / 8;
     const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -228,53 +268,99 @@ __global__ void __launch_bounds__(kLongThreads) row_int8_long_kernel(const RowAr
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, buf ^= 1) {
         const uint16_t* x = a.x + row * a.ldx;
         const uint16_t* res = kRes ? a.residual + row * a.ldr : nullptr;
+        uint16_t* out = kRes && a.residual_out ? a.residual_out + row * a.ldo : nullptr;
         float sum = 0.0f;
         uint32_t top = 0;
-        for (int v = threadIdx.x; v < vecs; v += kLongThreads) {
-            const int64_t at = 8 * static_cast<int64_t>(v);
-            float r[8], t[8];
-            sum_r<kRes>(ld_row16(x + at), kRes ? ld_row16(res + at) : zero, r);
-            weigh<kNorm>(kNorm ? *reinterpret_cast<const uint4*>(a.weight + at) : zero, a.weight_offset, r, t);
-            tally<kNorm>(r, t, sum, top);
+        for (int v0 = threadIdx.x; v0 < vecs; v0 += kLongThreads * kLongBatch) {
+            uint4 xv[kLongBatch], rv[kLongBatch];
+#pragma unroll
+            for (int j = 0; j < kLongBatch; ++j) {
+                const int64_t at = 8 * static_cast<int64_t>(v0 + j * kLongThreads);
+                if (v0 + j * kLongThreads < vecs) {
+                    xv[j] = ld_row16(x + at);
+                    rv[j] = kRes ? ld_row16(res + at) : zero;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kLongBatch; ++j) {
+                const int v = v0 + j * kLongThreads;
+                const int64_t at = 8 * static_cast<int64_t>(v);
+                if (v >= vecs) break;
+                if constexpr (kNorm) {
+                    const uint4 wv = *reinterpret_cast<const uint4*>(a.weight + at);
+                    float r[8], t[8];
+                    sum_r<kRes>(xv[j], rv[j], r);
+                    weigh<true>(wv, a.weight_offset, r, t);
+                    tally<true>(r, t, sum, top);
+                    if constexpr (kStaged) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            s_row[2 * v + i] = make_uint4(__float_as_uint(t[4 * i]), __float_as_uint(t[4 * i + 1]),
+                                                          __float_as_uint(t[4 * i + 2]), __float_as_uint(t[4 * i + 3]));
+                        if (out) *reinterpret_cast<uint4*>(out + at) = pack8(r);
+                    }
+                } else {
+                    top = tally16(xv[j], top);
+                    if constexpr (kStaged) s_row[v] = xv[j];
+                }
+            }
         }
-        reduce_row(sum, top, s_red[buf], kLongThreads / 32);
+        if constexpr (!kNorm) top = top_bits(top);
+        reduce_row<kNorm>(sum, top, s_red[buf], kLongThreads / 32);
         float mult;
         const bool ok = finish_row<kNorm>(a, row, sum, top, &mult);
         for (int v = threadIdx.x; v < vecs; v += kLongThreads) {
             const int64_t at = 8 * static_cast<int64_t>(v);
-            float r[8], t[8];
-            sum_r<kRes>(ld_row16(x + at), kRes ? ld_row16(res + at) : zero, r);
-            weigh<kNorm>(kNorm ? *reinterpret_cast<const uint4*>(a.weight + at) : zero, a.weight_offset, r, t);
-            if (kRes && a.residual_out) *reinterpret_cast<uint4*>(a.residual_out + row * a.ldo + at) = pack8(r);
+            float t[8];
+            if constexpr (kStaged && kNorm) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint4 q = s_row[2 * v + i];
+                    t[4 * i] = __uint_as_float(q.x), t[4 * i + 1] = __uint_as_float(q.y);
+                    t[4 * i + 2] = __uint_as_float(q.z), t[4 * i + 3] = __uint_as_float(q.w);
+                }
+            } else if constexpr (kStaged) {
+                sum_r<false>(s_row[v], zero, t);
+            } else {
+                // beyond shared memory: the row once more, from cache
+                float r[8];
+                sum_r<kRes>(ld_row16(x + at), kRes ? ld_row16(res + at) : zero, r);
+                if (out) *reinterpret_cast<uint4*>(out + at) = pack8(r);
+                if constexpr (kNorm) {
+                    weigh<true>(*reinterpret_cast<const uint4*>(a.weight + at), a.weight_offset, r, t);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) t[i] = r[i];
+                }
+            }
             *reinterpret_cast<uint2*>(a.codes + row * a.cols + at) = ok ? encode8(t, mult) : make_uint2(0, 0);
         }
     }
 }
 
-// `resident`: CTAs of `kern` per SM for each thread count in warps, 0 until
-// measured (racing threads measure the same value).
+// One kernel's launch state: CTAs per SM for each thread count in warps, 0
+// until measured (racing threads measure the same value).
 struct Resident {
     std::atomic<int> per_sm[kMaxDevices][33] = {};
 };
 
-nvfp4_status launch(void (*kern)(RowArgs), Resident& resident, int threads, const RowArgs& a, void* stream) {
-    DeviceInfo dev;
-    int id = 0;
-    nvfp4_status st = require_sm100(&dev);
-    if (st == NVFP4_OK) st = current_device(&id);
-    if (st != NVFP4_OK) return st;
+nvfp4_status launch(void (*kern)(RowArgs), std::atomic<int>& cached, int threads, int smem, const RowArgs& a,
+                    const DeviceInfo& dev, void* stream) {
     // resident CTAs only: each walks its share of the rows
-    std::atomic<int>& cached = resident.per_sm[id][threads / 32];
-    int per_sm = cached.load(std::memory_order_relaxed);
+    int per_sm = cached.load(std::memory_order_acquire);
     if (per_sm <= 0) {
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0) != cudaSuccess || per_sm <= 0)
+        if (smem > 0 &&
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLongSmem) != cudaSuccess)
             return NVFP4_ERR_CUDA;
-        cached.store(per_sm, std::memory_order_relaxed);
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem) != cudaSuccess || per_sm <= 0)
+            return NVFP4_ERR_CUDA;
+        cached.store(per_sm, std::memory_order_release);
     }
     const int64_t cap = static_cast<int64_t>(dev.sms) * per_sm;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows < cap ? a.rows : cap), 1, 1);
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = as_stream(stream);
     // a programmatic dependent: the kernels wait for the previous grid before
     // they touch global memory, so only their set-up overlaps it
@@ -287,15 +373,36 @@ nvfp4_status launch(void (*kern)(RowArgs), Resident& resident, int threads, cons
     return cuda_status(cudaGetLastError());
 }
 
+template <bool kNorm, bool kRes, int V>
+bool try_rows(const RowArgs& a, const DeviceInfo& dev, int id, void* stream, nvfp4_status* st) {
+    static Resident resident;
+    const int threads = ((a.cols / 8 + V - 1) / V + 31) / 32 * 32;
+    if (threads > row_max_threads(kNorm, V)) return false;
+    *st = launch(row_int8_kernel<kNorm, kRes, V>, resident.per_sm[id][threads / 32], threads, 0, a, dev, stream);
+    return true;
+}
+
 template <bool kNorm, bool kRes>
 nvfp4_status launch_rows(const RowArgs& a, void* stream) {
-    static Resident r2, r4, rl;
+    DeviceInfo dev;
+    int id = 0;
+    nvfp4_status st = require_sm100(&dev);
+    if (st == NVFP4_OK) st = current_device(&id);
+    if (st != NVFP4_OK) return st;
     // the fewest vectors per thread whose threads fit a CTA
-    const int vecs = a.cols / 8;
-    auto threads = [&](int v) { return ((vecs + v - 1) / v + 31) / 32 * 32; };
-    if (threads(2) <= row_max_threads(2)) return launch(row_int8_kernel<kNorm, kRes, 2>, r2, threads(2), a, stream);
-    if (threads(4) <= row_max_threads(4)) return launch(row_int8_kernel<kNorm, kRes, 4>, r4, threads(4), a, stream);
-    return launch(row_int8_long_kernel<kNorm, kRes>, rl, kLongThreads, a, stream);
+    if (try_rows<kNorm, kRes, 2>(a, dev, id, stream, &st)) return st;
+    if (try_rows<kNorm, kRes, 4>(a, dev, id, stream, &st)) return st;
+    if constexpr (!kNorm)
+        if (try_rows<kNorm, kRes, 8>(a, dev, id, stream, &st)) return st;
+    // CTAs per SM by the row's KB of shared memory
+    static std::atomic<int> staged[kMaxDevices][kLongSmem / 1024 + 1], unstaged[kMaxDevices];
+    const int64_t bytes = static_cast<int64_t>(a.cols) * (kNorm ? 4 : 2);
+    if (bytes <= kLongSmem) {
+        const int smem = static_cast<int>((bytes + 1023) / 1024 * 1024);
+        return launch(row_int8_long_kernel<kNorm, kRes, true>, staged[id][smem / 1024], kLongThreads, smem, a, dev,
+                      stream);
+    }
+    return launch(row_int8_long_kernel<kNorm, kRes, false>, unstaged[id], kLongThreads, 0, a, dev, stream);
 }
 
 // Same address and stride: every element is read by the thread that rewrites
@@ -341,8 +448,8 @@ extern "C" nvfp4_status nvfp4_add_rms_norm_int8(const void* x, int64_t ldx, cons
                                                 float* scale, void* stream) {
     if (rows < 0 || cols < 0) return NVFP4_ERR_INVALID_ARG;
     // a positive normal eps, so that an all-zero row has a finite factor
-    if (!(eps >= 0x1p-126f) || !(eps < 0x1p127f) || !(weight_offset > -0x1p127f) ||
-        !(weight_offset < 0x1p127f))
+    if (!(eps >= 0x1p-126f) || !(eps < 0x1p127f) || !(weight_offset > -0x1p100f) ||
+        !(weight_offset < 0x1p100f))
         return NVFP4_ERR_INVALID_ARG;
     if (!residual && residual_out) return NVFP4_ERR_INVALID_ARG;
     if (cols % 16 != 0 || ldx % 8 != 0 || (residual && ldr % 8 != 0) || (residual_out && ldo % 8 != 0))

@@ -56,7 +56,8 @@ def norm_args(**kw):
     (dict(weight=C + 8), ALIGN), (dict(residual_out=D + 8), ALIGN), (dict(codes=E + 8), ALIGN),
     (dict(scale=E + 0x100002), ALIGN), (dict(eps=0.0), ARG), (dict(eps=-1.0), ARG),
     (dict(eps=float("nan")), ARG), (dict(eps=float("inf")), ARG), (dict(eps=1e-39), ARG),
-    (dict(offset=float("nan")), ARG), (dict(offset=float("inf")), ARG),
+    (dict(offset=float("nan")), ARG), (dict(offset=float("inf")), ARG), (dict(offset=2.0 ** 100), ARG),
+    (dict(offset=-2.0 ** 100), ARG),
     (dict(rows=1 << 40, ldx=1 << 20), SHAPE), (dict(rows=1 << 40, ldr=1 << 20), SHAPE),
     (dict(residual_out=A + 16), ARG), (dict(residual_out=B, ldo=72), ARG), (dict(residual_out=C), ARG),
     (dict(codes=A), ARG), (dict(codes=B), ARG), (dict(codes=C), ARG), (dict(codes=D), ARG),
