@@ -744,6 +744,10 @@ PROFILE_CASES = {
     "global_scale_act": "global scale of the activation [32768,5120]",
     "kv_quantize": "FP8 E4M3 KV cache: BF16 [65536,2048] -> bytes, calibrated per-tensor scale",
     "harmonize_gdn": "harmonisation of the fused GDN weight's scales [24704,5120], in place",
+    "int8_gemm_gateup": "int8 GEMM, A [8192,5120] x W [34816,5120]",
+    "int8_gemm_decode": "int8 GEMM, A [8,5120] x W [34816,5120]",
+    "int8_norm": "residual addition, RMS norm and int8 codes of [32768,5120]",
+    "int8_quantize": "int8 codes of the MLP intermediate [8192,17408]",
 }
 
 
@@ -796,6 +800,28 @@ def run_profile_case(case: str, launches: int) -> None:
         torch.cuda.synchronize()
         for _ in range(launches):
             nv.harmonize(fw)
+    elif case in ("int8_gemm_gateup", "int8_gemm_decode"):
+        M = 8192 if case == "int8_gemm_gateup" else 8
+        a = nv.int8_quantize_tensor(synth.student_t_activations(M, K_HID, seed=1, device=dev))
+        w = nv.int8_quantize_tensor(synth.gaussian_weights(34816, K_HID, 0.015, seed=20, device=dev))
+        y = torch.empty(M, 34816, dtype=torch.bfloat16, device=dev)
+        torch.cuda.synchronize()
+        for _ in range(launches):
+            nv.int8_gemm(a, w, y)
+    elif case == "int8_norm":
+        x = synth.student_t_activations(32768, K_HID, seed=1, device=dev)
+        res = synth.student_t_activations(32768, K_HID, seed=2, device=dev)
+        weight = torch.ones(K_HID, dtype=torch.bfloat16, device=dev)
+        q, out = nv.add_rms_norm_int8(x, weight, residual=res)
+        torch.cuda.synchronize()
+        for _ in range(launches):
+            nv.add_rms_norm_int8(x, weight, residual=res, residual_out=out, codes=q.codes, scale=q.scale)
+    elif case == "int8_quantize":
+        x = synth.student_t_activations(8192, 17408, seed=1, device=dev)
+        codes, scale = nv.int8_quantize(x)
+        torch.cuda.synchronize()
+        for _ in range(launches):
+            nv.int8_quantize(x, codes, scale)
     else:
         raise SystemExit(f"unknown profile case {case!r}; cases: {', '.join(PROFILE_CASES)}")
     torch.cuda.synchronize()

@@ -617,23 +617,27 @@ def _stream_handle(index: int, stream) -> int:
 
 
 def _check_codes(t, name: str, shape=None):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int8 or t.dim() != 2 or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype is not _I8 or t.dim() != 2 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 2-D int8 tensor")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _check_row_scale(t, name: str, rows: int):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_contiguous() \
+    if not isinstance(t, torch.Tensor) or t.dtype is not _F32 or not t.is_contiguous() \
             or t.numel() != rows:
         raise ValueError(f"{name} must be a contiguous float32 tensor of {rows} elements")
 
 
 # The three calls below take a few microseconds on the device for a decode
-# step, so the device check of a correct call reads device indices only (an
-# outsider sends it to _check_devices, which names the tensor), the stream is
-# taken by its handle, and a single row's stride, which torch may report as
-# anything, is given as the row's length rounded up to 8.
+# step.  So a correct call is recognised with few attribute reads, and only one
+# that is not goes through the checks that name the tensor; the stream is taken
+# by its handle; and a single row's stride, which torch may report as anything,
+# is given as the row's length rounded up to 8.
+_BF16, _I8, _F32 = torch.bfloat16, torch.int8, torch.float32
+_current_device = torch.cuda.current_device
+
+
 def int8_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
                   scale: Optional[torch.Tensor] = None, stream=None):
     """int8 codes [rows, cols] and FP32 scales [rows] of a BF16 matrix:
@@ -641,7 +645,7 @@ def int8_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
     _check_bf16_matrix(x, "x")
     rows, cols = x.shape
     dev = x.get_device()
-    same = dev >= 0 and dev == torch.cuda.current_device()
+    same = dev >= 0 and dev == _current_device()
     if codes is not None:
         _check_codes(codes, "codes", x.shape)
         same = same and codes.get_device() == dev
@@ -651,9 +655,9 @@ def int8_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
     if not same:
         _check_devices(x=x, codes=codes, scale=scale)
     if codes is None:
-        codes = _empty(rows, cols, dtype=torch.int8, device=x.device, stream=stream)
+        codes = _empty(rows, cols, dtype=_I8, device=x.device, stream=stream)
     if scale is None:
-        scale = _empty(rows, dtype=torch.float32, device=x.device, stream=stream)
+        scale = _empty(rows, dtype=_F32, device=x.device, stream=stream)
     st = _lib.lib().nvfp4_int8_quantize(
         x.data_ptr(), rows, cols, x.stride(0) if rows > 1 else (cols + 7) // 8 * 8, codes.data_ptr(),
         scale.data_ptr(), _stream_handle(dev, stream))
@@ -678,19 +682,20 @@ def add_rms_norm_int8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[
     quantized per row.  Returns (Int8Tensor of v, r in BF16); the second is
     None without a residual.  residual_out may be residual or x (in place)."""
     _check_bf16_matrix(x, "x")
-    rows, cols = x.shape
-    if not isinstance(weight, torch.Tensor) or weight.dtype != torch.bfloat16 \
+    shape = x.shape
+    rows, cols = shape
+    if not isinstance(weight, torch.Tensor) or weight.dtype is not _BF16 \
             or weight.shape != (cols,) or not weight.is_contiguous():
         raise ValueError(f"weight must be a contiguous bfloat16 tensor of {cols} elements")
     dev = x.get_device()
-    same = dev >= 0 and dev == torch.cuda.current_device() and weight.get_device() == dev
+    same = dev >= 0 and dev == _current_device() and weight.get_device() == dev
     if residual is not None:
         _check_bf16_matrix(residual, "residual")
-        if residual.shape != x.shape:
-            raise ValueError(f"residual must have shape {tuple(x.shape)}, got {tuple(residual.shape)}")
+        if residual.shape != shape:
+            raise ValueError(f"residual must have shape {tuple(shape)}, got {tuple(residual.shape)}")
         same = same and residual.get_device() == dev
         if residual_out is not None:
-            _check_out_matrix(residual_out, "residual_out", torch.bfloat16, rows, cols)
+            _check_out_matrix(residual_out, "residual_out", _BF16, rows, cols)
             same = same and residual_out.get_device() == dev
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
@@ -705,14 +710,14 @@ def add_rms_norm_int8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[
                        scale=scale)
     device = x.device
     if codes is None:
-        codes = _empty(rows, cols, dtype=torch.int8, device=device, stream=stream)
+        codes = _empty(rows, cols, dtype=_I8, device=device, stream=stream)
     if scale is None:
-        scale = _empty(rows, dtype=torch.float32, device=device, stream=stream)
+        scale = _empty(rows, dtype=_F32, device=device, stream=stream)
     one = (cols + 7) // 8 * 8 if rows <= 1 else 0
     r = ldr = out = ldo = 0
     if residual is not None:
         if residual_out is None:
-            residual_out = _empty(rows, cols, dtype=torch.bfloat16, device=device, stream=stream)
+            residual_out = _empty(rows, cols, dtype=_BF16, device=device, stream=stream)
         r, ldr = residual.data_ptr(), one or residual.stride(0)
         out, ldo = residual_out.data_ptr(), one or residual_out.stride(0)
     st = _lib.lib().nvfp4_add_rms_norm_int8(
@@ -738,16 +743,16 @@ def int8_gemm(a: Int8Tensor, w: Int8Tensor, y: Optional[torch.Tensor] = None,
     _check_row_scale(asc, "a.scale", M)
     _check_row_scale(wsc, "w.scale", N)
     dev = ac.get_device()
-    same = dev >= 0 and dev == torch.cuda.current_device() and \
+    same = dev >= 0 and dev == _current_device() and \
         asc.get_device() == wc.get_device() == wsc.get_device() == dev
     if y is not None:
-        _check_out_matrix(y, "y", torch.bfloat16, M, N)
+        _check_out_matrix(y, "y", _BF16, M, N)
         same = same and y.get_device() == dev
     if not same:
         _check_devices(a_codes=ac, a_scale=asc, w_codes=wc, w_scale=wsc, y=y)
     ldy = (N + 7) // 8 * 8
     if y is None:
-        y = _empty(M, ldy, dtype=torch.bfloat16, device=ac.device, stream=stream)
+        y = _empty(M, ldy, dtype=_BF16, device=ac.device, stream=stream)
         if ldy != N:
             y = y[:, :N]
     elif M > 1:
