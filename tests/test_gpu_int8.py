@@ -299,6 +299,25 @@ def test_gemm_output_widths(M, N):
     assert_gemm(a, w, y)
 
 
+@pytest.mark.parametrize("M,N,K", [
+    # few tokens: tile widths and stage depths from one step to eight, rounds
+    # of tiles, K that ends inside a stage, a step and an instruction
+    (128, 24640, 1040), (128, 24640, 1024), (100, 34816, 640), (8, 34816, 1152), (1, 40000, 1280),
+    (64, 5120, 1168), (16, 2048, 3200), (33, 151936, 128), (128, 40, 17408),
+    # CTA pairs: every tile width, several rounds, bands of M tiles
+    (200, 5120, 272), (300, 5120, 272), (200, 24640, 272), (520, 24640, 400), (257, 19000, 144),
+    (1000, 5120, 272), (2048, 5120, 144), (260, 151936, 64), (4200, 200, 13008)])
+def test_gemm_configurations(M, N, K):
+    a, w = gemm_inputs(M, N, K, seed=M + K)
+    y = nv.int8_gemm(a, w)
+    torch.cuda.synchronize()
+    assert nv.last_device_status() == 0
+    # exact sums in 64 bits, then the three roundings
+    acc = a.codes.double() @ w.codes.double().t()
+    want = (acc.float() * a.scale[:, None] * w.scale[None, :]).to(BF)
+    assert torch.equal(y, want)
+
+
 @pytest.mark.parametrize("M", [1, 5, 129, 300])
 @pytest.mark.parametrize("fill", [(-128, -128), (127, -128), (127, 127)])
 def test_gemm_largest_sums(M, fill):
@@ -514,6 +533,49 @@ def test_calls_on_other_streams(M):
             outs.append(nv.linear(x, w, stream=s)[:0])
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs if o.shape[0])
+
+
+@pytest.mark.parametrize("M", [1, 270])
+def test_calls_behind_a_long_kernel(M):
+    # the kernels are let in early and wait for the previous grid; their bounded
+    # waits must not run meanwhile
+    H = 512
+    x, res, nw = norm_inputs(M, H, True, 0, 0.0, seed=1)
+    w = nv.int8_quantize_tensor(synth.gaussian_weights(H, H, 0.03, seed=4, device=DEV))
+    want = nv.linear(nv.add_rms_norm_int8(x, nw, residual=res)[0], w)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(3_000_000_000)                 # about 1.5 s
+    got = nv.linear(nv.add_rms_norm_int8(x, nw, residual=res)[0], w)
+    torch.cuda.synchronize()
+    assert nv.last_device_status() == 0 and torch.equal(got, want)
+
+
+def test_few_token_and_prefill_products_at_once():
+    small, w = gemm_inputs(3, 5120, 2048, seed=1)
+    big, _ = gemm_inputs(700, 8, 2048, seed=2)
+    want = nv.int8_gemm(small, w), nv.int8_gemm(big, w)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [(nv.int8_gemm(small, w, stream=s1), nv.int8_gemm(big, w, stream=s2)) for _ in range(20)]
+    torch.cuda.synchronize()
+    assert nv.last_device_status() == 0
+    assert all(torch.equal(a, want[0]) and torch.equal(b, want[1]) for a, b in got)
+
+
+def test_single_rows_of_any_stride_and_refused_strides():
+    buf = activations(3, 104, seed=5)
+    odd = torch.empty(3 * 100 + 8, dtype=BF, device=DEV)[:300].view(3, 100)
+    odd.copy_(buf[:, :100])
+    x = odd[:1, :64]                                  # a row stride that is no multiple of 8
+    codes_, scale = nv.int8_quantize(x)
+    q, r = nv.add_rms_norm_int8(x, torch.ones(64, dtype=BF, device=DEV), residual=x)
+    torch.cuda.synchronize()
+    want_c, want_s = ref.quantize(f32(x))
+    assert same(codes_.cpu(), want_c) and same(f32(scale), want_s)
+    assert_norm(x, x, torch.ones(64, dtype=BF), 0.0, 1e-6, q, r)
+    for bad in (odd[:2, :64], buf[:1, :64].expand(4, 64), buf[:, 4:68]):
+        with pytest.raises(nv.Nvfp4Error):
+            nv.int8_quantize(bad)
 
 
 def test_saved_and_loaded_weight_serves_the_same(tmp_path):
