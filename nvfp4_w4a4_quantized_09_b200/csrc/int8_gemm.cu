@@ -36,8 +36,11 @@ constexpr uint64_t kTimeoutNs = 1000000000ull;  // 1 s per wait
 __device__ __forceinline__ float scale_f32(int32_t acc, float sa, float sw) {
     return __fmul_rn(__fmul_rn(__int2float_rn(acc), sa), sw);
 }
-__device__ __forceinline__ uint16_t scale_bf16(int32_t acc, float sa, float sw) {
-    return __bfloat16_as_ushort(__float2bfloat16_rn(scale_f32(acc, sa, sw)));
+// Two neighbouring values as packed BF16 (the low half first).
+__device__ __forceinline__ uint32_t scale_bf16x2(uint32_t acc0, uint32_t acc1, float sa, float sw0, float sw1) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(scale_f32(static_cast<int32_t>(acc0), sa, sw0),
+                                                   scale_f32(static_cast<int32_t>(acc1), sa, sw1));
+    return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 constexpr int kEpiWarps = 8;                    // two per TMEM lane quarter
@@ -168,8 +171,18 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
     const bool leader = elect_one();
     if (warp == 0) {
         // ---------------- TMA producer (both CTAs) ----------------
+        // With one M tile the weight streams from memory once, as for few
+        // tokens: while the previous grid finishes, its first ring moves into
+        // L2 (a hint: nothing of it is read before the wait).
+        const bool once = args.m_tiles == 1;
+        if (leader && once) {
+            const int ahead = min(STAGES, args.k_steps);
+            for (int kb = 0; kb < ahead; ++kb)
+                tma_prefetch_2d(&tmap_b, kb * kStepBytes, pair * BN + static_cast<int>(rank) * (BN / 2));
+        }
         grid_dependency_wait();
         const uint64_t pol = l2_policy_evict_last();
+        const uint64_t pol_w = once ? l2_policy_evict_first() : pol;
         int stage = 0;
         uint32_t phase = 0;
         uint32_t armed = 0, armed_parity = 0;   // stages the even CTA expects bytes on
@@ -188,7 +201,7 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 if (leader && !failed) {
                     if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (A_BYTES + B_BYTES));
                     tma_load_2d_pair(smem + stage * A_BYTES, &tmap_a, fb, kb * kStepBytes, ya, pol);
-                    tma_load_2d_pair(smem + off_b + stage * B_BYTES, &tmap_b, fb, kb * kStepBytes, yb, pol);
+                    tma_load_2d_pair(smem + off_b + stage * B_BYTES, &tmap_b, fb, kb * kStepBytes, yb, pol_w);
                 }
                 __syncwarp();
                 if (rank == 0 && !failed) {
@@ -306,12 +319,8 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     uint32_t o[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const float v0 = scale_f32(static_cast<int32_t>(r[2 * j]), sa,
-                                                   __shfl_sync(0xFFFFFFFFu, sw[i], 2 * j));
-                        const float v1 = scale_f32(static_cast<int32_t>(r[2 * j + 1]), sa,
-                                                   __shfl_sync(0xFFFFFFFFu, sw[i], 2 * j + 1));
-                        o[j] = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(v0))) |
-                               (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(v1))) << 16);
+                        o[j] = scale_bf16x2(r[2 * j], r[2 * j + 1], sa, __shfl_sync(0xFFFFFFFFu, sw[i], 2 * j),
+                                            __shfl_sync(0xFFFFFFFFu, sw[i], 2 * j + 1));
                     }
                     if (n0 + 32 > args.N && (args.N & 7) != 0) {       // warp-uniform
                         // TMA stores whole 16-byte pieces of a row: columns
@@ -472,13 +481,13 @@ nvfp4_status launch_few(const Operands& o, const DeviceInfo& info, int* status, 
     f.k_steps = (o.K + kStepBytes - 1) / kStepBytes;
     f.timeout_ns = kTimeoutNs;
     f.status = status;
-    // Tile width.  Over all rounds of tiles an SM spends on each k-step the
-    // larger of its MMAs (four of BN / 2 cycles, 52 at the least, and 230 for a
-    // stage's handshake) and its feed (about 42 bytes a cycle while all SMs
-    // stream); memory as a whole delivers some 3400 bytes of weights a cycle.
-    // The slower of the two decides; a quarter of the SMs' share is added, so
-    // that among widths that memory bounds the least loaded SMs win, and the
-    // narrowest among equals.
+    // Tile width, by cycles.  Over all rounds of tiles an SM spends on each
+    // k-step the larger of its MMAs (four of BN / 2, 52 at the least, and 230
+    // for a stage's handshake) and its feed (about 42 bytes a cycle while all
+    // SMs stream); memory as a whole delivers some 3400 bytes of weights a
+    // cycle.  The slower of the two decides; a quarter of the SMs' share is
+    // added, so that among widths that memory bounds the least loaded SMs win,
+    // and the last tile's epilogue (225 a chunk of a warp's 16 channels).
     int u = 0;
     int64_t best = 0;
     const int64_t memory = o.N * static_cast<int64_t>(kStepBytes) / 3400;
@@ -488,7 +497,7 @@ nvfp4_status launch_few(const Operands& o, const DeviceInfo& info, int* status, 
         few_config(f.nt, bn, &bu, &bs);
         const int64_t sm = (tiles + info.sms - 1) / info.sms *
                            std::max(4 * std::max(52, bn / 2) + 230 / bu, (f.nt + bn) * kStepBytes / 42);
-        const int64_t cost = 4 * std::max(sm, memory) + sm;
+        const int64_t cost = f.k_steps * (std::max(sm, memory) + sm / 4) + (bn + 31) / 32 * 225;
         if (best == 0 || cost < best) best = cost, f.bn = bn, f.stages = bs, u = bu;
     }
     f.n_tiles = (o.N + f.bn - 1) / f.bn;

@@ -25,7 +25,8 @@ constexpr int kFewMaxStages = 16;
 constexpr int kFewMaxBN = 256;
 constexpr uint32_t kFewSmem = 227 * 1024;            // whole: one CTA per SM
 constexpr uint32_t kFewBars = (2 * kFewMaxStages + 5) * 8;
-constexpr uint32_t kFewRing = (kFewSmem - 1024 - kFewBars - 16) / 1024 * 1024;
+constexpr uint32_t kFewScales = 2 * kFewMaxBN * 4;    // channel scales, one set per accumulator
+constexpr uint32_t kFewRing = (kFewSmem - 1024 - kFewBars - kFewScales - 16) / 1024 * 1024;
 
 struct FewArgs {
     const float* sa;
@@ -78,7 +79,8 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
     const uint32_t a_step = static_cast<uint32_t>(args.nt) * kStepBytes;
     const uint32_t b_step = static_cast<uint32_t>(BN) * kStepBytes;
     const uint32_t off_b = static_cast<uint32_t>(STAGES * U) * a_step;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kFewRing);
+    float* s_scales = reinterpret_cast<float*>(smem + kFewRing);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kFewRing + kFewScales);
     uint64_t* empty = full + kFewMaxStages;
     uint64_t* tmem_full = empty + kFewMaxStages;        // [2]
     uint64_t* tmem_empty = tmem_full + 2;               // [2]
@@ -255,56 +257,54 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
         __syncwarp();
     } else {
         // ---------------- epilogue (warps 2..9) ----------------
-        // lane -> token; 16 channels at a time, a 32-byte sector of the row
+        // lane -> token; 16 channels at a time, a 32-byte sector of the row, the
+        // next chunk's TMEM load under way meanwhile.  The channels' scales pass
+        // through shared memory while the MMAs run.
+        constexpr int kChunks = kFewMaxBN / 32;       // per warp
         const int q = warp & 3;                       // TMEM lane quarter of this warp
         const int half = (warp - 2) >> 2;
-        constexpr int kChunks = kFewMaxBN / 32;       // per warp
         const int m0 = q * 32;
-        const uint32_t tq = tmem_base + (static_cast<uint32_t>(m0) << 16);
+        const uint32_t tq = tmem_base + (static_cast<uint32_t>(m0) << 16) + half * 16;
+        const int tid = threadIdx.x - 64;
         grid_dependency_wait();
         const float sa = m0 + lane < args.M ? args.sa[m0 + lane] : 0.0f;
         uint16_t* yrow = args.y + static_cast<int64_t>(m0 + lane) * args.ldy;
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int nt = blockIdx.x; nt < args.n_tiles; nt += gridDim.x) {
-            // the tile's channel scales are on their way while the MMAs run
-            float sw[kChunks];
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                const int c = half * 16 + 32 * i + (lane & 15);
-                sw[i] = m0 < args.M && c < BN && nt * BN + c < args.N ? args.sw[nt * BN + c] : 0.0f;
-            }
+            float* s_sw = s_scales + acc * kFewMaxBN;  // last read two tiles ago, before the previous barrier
+            s_sw[tid] = nt * BN + tid < args.N && tid < BN ? args.sw[nt * BN + tid] : 0.0f;
+            named_barrier_sync(1, 32 * kEpiWarps);
             if (!mbar_wait_warp(&tmem_full[acc], acc_phase, args.timeout_ns, s_abort, args.status)) break;
             tc_fence_after();
-            if (m0 < args.M) {                                         // warp-uniform
+            // columns of the tile inside the matrix, in chunks of this warp
+            const int cols = min(BN, args.N - nt * BN) - half * 16;
+            const int nch = m0 < args.M && cols > 0 ? (cols + 31) / 32 : 0;   // warp-uniform
+            const uint32_t src = tq + acc * 256;
+            uint32_t r[2][16];
+            if (nch > 0) tmem_ld_16cols(src, r[0]);
 #pragma unroll
-                for (int i = 0; i < kChunks; ++i) {
-                    const int c = half * 16 + 32 * i;
-                    const int n0 = nt * BN + c;
-                    if (c >= BN || n0 >= args.N) break;                // warp-uniform
-                    uint32_t r[16];
-                    tmem_ld_16cols(tq + acc * 256 + c, r);
-                    tmem_ld_wait();
-                    uint32_t o[8];
+            for (int i = 0; i < kChunks; ++i) {
+                if (i >= nch) break;
+                tmem_ld_wait();
+                if (i + 1 < nch) tmem_ld_16cols(src + 32 * (i + 1), r[(i + 1) & 1]);
+                const int c = half * 16 + 32 * i, n0 = nt * BN + c;
+                uint32_t o[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t lo = scale_bf16(static_cast<int32_t>(r[2 * j]), sa,
-                                                       __shfl_sync(0xFFFFFFFFu, sw[i], 2 * j));
-                        const uint32_t hi = scale_bf16(static_cast<int32_t>(r[2 * j + 1]), sa,
-                                                       __shfl_sync(0xFFFFFFFFu, sw[i], 2 * j + 1));
-                        o[j] = lo | (hi << 16);
-                    }
-                    if (m0 + lane < args.M) {
-                        uint16_t* yp = yrow + n0;
-                        if (n0 + 16 <= args.N) {
-                            *reinterpret_cast<uint4*>(yp) = make_uint4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<uint4*>(yp + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-                        } else {
+                for (int j = 0; j < 4; ++j) {
+                    const float4 w4 = *reinterpret_cast<const float4*>(s_sw + c + 4 * j);
+                    o[2 * j] = scale_bf16x2(r[i & 1][4 * j], r[i & 1][4 * j + 1], sa, w4.x, w4.y);
+                    o[2 * j + 1] = scale_bf16x2(r[i & 1][4 * j + 2], r[i & 1][4 * j + 3], sa, w4.z, w4.w);
+                }
+                if (m0 + lane < args.M) {
+                    uint16_t* yp = yrow + n0;
+                    if (n0 + 16 <= args.N) {
+                        *reinterpret_cast<uint4*>(yp) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4*>(yp + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                    } else {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (n0 + j < args.N)
-                                    yp[j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
-                        }
+                        for (int j = 0; j < 16; ++j)
+                            if (n0 + j < args.N) yp[j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
                     }
                 }
             }

@@ -85,6 +85,10 @@ __device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity, uint32_
 // Bring a box into L2, a hint that nothing waits for.  L2 is where this GPU's
 // memory is coherent, so a box that an earlier kernel is still writing may be
 // prefetched: the later load reads what that kernel wrote.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int32_t x, int32_t y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y)
+                 : "memory");
+}
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int32_t x, int32_t y, int32_t z) {
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x),
                  "r"(y), "r"(z)
