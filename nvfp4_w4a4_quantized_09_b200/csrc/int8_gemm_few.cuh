@@ -1,19 +1,34 @@
 // int8_gemm_few.cuh -- the int8 GEMM for few tokens (M <= 128), where the
 // weight streams from memory once.  Included by int8_gemm.cu.
 //
-//   * One CTA per tile of all the tokens x BN channels (MMA M = 128, N = BN, a
-//     multiple of 16 up to 256).  BN is free, so the launcher picks it to fill
-//     whole rounds of the SMs: no split of K, no partial sums.
-//   * Only the tokens' own rows are loaded (NT = M rounded up to 8).  The MMA
-//     reads 128 rows from the tile's start; the rows beyond NT are whatever
-//     shared memory holds there, and the accumulator lanes they fill are never
-//     read.
+// One CTA per tile of all the tokens x BN channels, in one of two ways:
+//   * M > 32: the tokens are the MMA's 128 rows and the channels its N = BN, a
+//     multiple of 16 up to 256.  BN is free, so the launcher picks it to fill
+//     whole rounds of the SMs: no split of K, no partial sums.  Only the
+//     tokens' own rows are loaded (NT = M rounded up to 8); the MMA reads 128
+//     rows from the tile's start, those beyond NT are whatever shared memory
+//     holds there, and the accumulator lanes they fill are never read.
+//   * M <= 32 (kSwap): the channels are the MMA's 64 or 128 rows and the tokens
+//     its N = 16 or 32.  The same weight bytes then take an eighth to a quarter
+//     of the multiplications, and with them of the power: the first form drives
+//     the SM clock down to 1.5 GHz when such products run back to back (8 x
+//     34816 x 5120: 32.7 us in a long run against 27.7 in a short one; swapped
+//     28.1 and 27.5).  From some 40 tokens on the free BN gains more (64 x
+//     24640 x 5120: 24.1 us against 26.8 swapped, long runs).
+// Common to both:
 //   * A pipeline stage holds U = 1, 2, 4 or 8 steps of 128 values of K, the
 //     most that 58 KB take: each stage costs the MMA warp a handshake during
 //     which the tensor pipe idles, and each operand one copy.
 //   * Persistent: the ring runs across tiles, two accumulators of 256 columns.
 //   * Launched as a programmatic dependent: every role that touches global
-//     memory first waits for the previous grid (griddepcontrol.wait).
+//     memory first waits for the previous grid (griddepcontrol.wait); the
+//     first ring of weights is prefetched into L2 before that (5 to 7 % of a
+//     call, measured for 24640 and 34816 channels).
+// Bound by memory: 8 x 34816 x 5120 27.5 us = 6.5 TB/s, 1 x 24640 x 5120 21.0 us
+// = 6.0 TB/s, 100 x 24640 x 5120 22.4 us = 5.9 TB/s, 8 x 151936 x 5120 115 us =
+// 6.8 TB/s (CUDA-graph replay).  Small products are bound by what a launch
+// costs around its stream: 16 x 2048 x 2048 4.2 us, 1 x 5120 x 5120 8.2 us for
+// 26 MB.
 //
 // Roles (10 warps): 0 TMA producer; 1 TMEM owner and MMA issuer; 2..9 epilogue,
 // two warps per TMEM lane quarter on alternate 16-column chunks.  Every wait is
@@ -21,6 +36,7 @@
 
 constexpr int kFewThreads = 320;
 constexpr int kFewMaxTokens = 128;
+constexpr int kSwapTokens = 32;                      // at most: channels as the MMA's rows
 constexpr int kFewMaxStages = 16;
 constexpr int kFewMaxBN = 256;
 constexpr uint32_t kFewSmem = 227 * 1024;            // whole: one CTA per SM
@@ -35,7 +51,7 @@ struct FewArgs {
     int64_t ldy;
     int M, N, K;
     int n_tiles, k_steps;
-    int nt;          // token rows loaded: M rounded up to 8
+    int nt;          // token rows loaded: M rounded up to 8 (16 when swapped)
     int bn;          // channels per tile
     int wide;        // one copy brings a stage's U steps of an operand
     int stages;
@@ -53,10 +69,10 @@ __host__ __device__ constexpr void few_config(int nt, int bn, int* u, int* stage
     *stages = st > kFewMaxStages ? kFewMaxStages : st;
 }
 
-// Every shape keeps at least three stages, and the MMA's 128 rows from the last
-// A tile's start end inside the ring (the B tiles follow the A tiles).
+// Every shape keeps at least three stages, and the MMA's 128 token rows from
+// the last A tile's start end inside the ring (the B tiles follow the A tiles).
 constexpr bool few_configs_fit() {
-    for (int nt = 8; nt <= kFewMaxTokens; nt += 8)
+    for (int nt = 16; nt <= kFewMaxTokens; nt += 8)
         for (int bn = 16; bn <= kFewMaxBN; bn += 16) {
             int u = 0, st = 0;
             few_config(nt, bn, &u, &st);
@@ -68,7 +84,7 @@ constexpr bool few_configs_fit() {
 static_assert(few_configs_fit(), "a few-token configuration does not fit");
 static_assert(kFewSmem > 228 * 1024 / 2, "two CTAs could share an SM and its 512 TMEM columns");
 
-template <int U>
+template <int U, bool kSwap>
 __global__ void __launch_bounds__(kFewThreads, 1)
 int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
                      const __grid_constant__ CUtensorMap tmap_w, const FewArgs args) {
@@ -195,9 +211,12 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
         // nothing here reads memory; the bounded waits below begin when the
         // previous grid, however long it takes, has finished
         grid_dependency_wait();
-        const uint32_t idesc = int8_idesc(kRows, BN);
-        const uint64_t da0 = sdesc_kmajor_sw128(smem_u32(smem));
-        const uint64_t db0 = sdesc_kmajor_sw128(smem_u32(smem + off_b));
+        // D's rows are the tokens, or with kSwap the channels
+        const uint32_t idesc = kSwap ? int8_idesc(BN, args.nt) : int8_idesc(kRows, BN);
+        const uint64_t da0 = sdesc_kmajor_sw128(smem_u32(kSwap ? smem + off_b : smem));
+        const uint64_t db0 = sdesc_kmajor_sw128(smem_u32(kSwap ? smem : smem + off_b));
+        const uint32_t da_step = (kSwap ? b_step : a_step) >> 4;
+        const uint32_t db_step = (kSwap ? a_step : b_step) >> 4;
         const int last_n = (args.K - (k_stages - 1) * U * kStepBytes + 31) / 32;   // MMAs of the last stage
         const uint32_t acc_empty0 = smem_u32(tmem_empty);
         bool failed = false;
@@ -215,22 +234,22 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
                 ready = mbar_peek(full0 + 8 * next, next_phase);
                 // descriptor start addresses advance by 2 per 32 bytes of K
-                const uint64_t da = da0 + static_cast<uint64_t>(stage * U) * (a_step >> 4);
-                const uint64_t db = db0 + static_cast<uint64_t>(stage * U) * (b_step >> 4);
+                const uint64_t da = da0 + static_cast<uint64_t>(stage * U) * da_step;
+                const uint64_t db = db0 + static_cast<uint64_t>(stage * U) * db_step;
                 if (leader && !failed) {
                     if (ks + 1 < k_stages) {
 #pragma unroll
                         for (int i = 0; i < U; ++i)
 #pragma unroll
                             for (int j = 0; j < kStepBytes / 32; ++j)
-                                tc_mma_i8(d_tmem, da + i * (a_step >> 4) + 2 * j, db + i * (b_step >> 4) + 2 * j,
-                                          idesc, static_cast<uint32_t>(ks | i | j));
+                                tc_mma_i8(d_tmem, da + i * da_step + 2 * j, db + i * db_step + 2 * j, idesc,
+                                          static_cast<uint32_t>(ks | i | j));
                     } else {
                         // the last stage ends with K
                         for (int i = 0; i < last_n; ++i) {
                             const uint32_t j = 2 * (i & 3);
-                            tc_mma_i8(d_tmem, da + (i >> 2) * (a_step >> 4) + j, db + (i >> 2) * (b_step >> 4) + j,
-                                      idesc, static_cast<uint32_t>(ks | i));
+                            tc_mma_i8(d_tmem, da + (i >> 2) * da_step + j, db + (i >> 2) * db_step + j, idesc,
+                                      static_cast<uint32_t>(ks | i));
                         }
                     }
                     tc_commit(&empty[stage]);
@@ -255,6 +274,47 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
             mbar_wait_bounded(drain, 0, args.timeout_ns, &local_abort, args.status);
         }
         __syncwarp();
+    } else if constexpr (kSwap) {
+        // ---------------- epilogue (warps 2..9), rows of D are channels ----------------
+        // lane -> channel, 16 tokens at a time; a warp's stores of one token are
+        // consecutive in memory.  128 channels fill the TMEM lanes, 64 the first
+        // 16 of each quarter.
+        const int q = warp & 3;
+        const int half = (warp - 2) >> 2;
+        const int tid = threadIdx.x - 64;
+        const int per_q = BN / 4;
+        const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+        grid_dependency_wait();
+        if (tid < args.M) s_scales[tid] = args.sa[tid];
+        named_barrier_sync(1, 32 * kEpiWarps);
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int nt = blockIdx.x; nt < args.n_tiles; nt += gridDim.x) {
+            const int n = nt * BN + q * per_q + lane;
+            const bool mine = lane < per_q && n < args.N;
+            const float sw = mine ? args.sw[n] : 0.0f;      // on its way while the MMAs run
+            if (!mbar_wait_warp(&tmem_full[acc], acc_phase, args.timeout_ns, s_abort, args.status)) break;
+            tc_fence_after();
+            for (int c = half * 16; c < args.M; c += 32) {
+                uint32_t r[16];
+                tmem_ld_16cols(tq + acc * 256 + c, r);
+                tmem_ld_wait();
+                if (mine) {
+                    uint16_t* yp = args.y + static_cast<int64_t>(c) * args.ldy + n;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (c + j < args.M)
+                            yp[j * args.ldy] = __bfloat16_as_ushort(__float2bfloat16_rn(
+                                scale_f32(static_cast<int32_t>(r[j]), s_scales[c + j], sw)));
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tmem_empty[acc]);
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        }
     } else {
         // ---------------- epilogue (warps 2..9) ----------------
         // lane -> token; 16 channels at a time, a 32-byte sector of the row, the
