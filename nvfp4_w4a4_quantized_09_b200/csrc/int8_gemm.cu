@@ -61,6 +61,15 @@ constexpr int kEpiWarps = 8;                    // two per TMEM lane quarter
 //               32-column chunks: scales, BF16, a 32 x 32 tile staged in the
 //               64-byte swizzle and one TMA store of it (rows beyond M and
 //               whole 16-byte pieces beyond N clipped by the tensor map)
+// 8192 x 34816 x 5120 takes 780 us by itself (3.74 P op/s; the tensor pipe is
+// busy 97 % of the SMs' active time) and 955 to 1000 us back to back, where the
+// power limit holds the SMs at some 1.3 GHz.  Smaller products are bound by
+// shared memory, which the copies' writes and the MMAs' reads share, and by how
+// the tiles fill the rounds: 1000 x 5120 x 17408 (128 tiles of 160 columns on 74
+// pairs) 69 us, 512 x 24640 x 5120 48 us, 200 x 24640 x 5120 30 us, 517 x 2051 x
+// 1040 6.7 us.  Six stages of 32 KB against five: 1000 and 1062 us for the
+// largest; spinning feed waits against suspending ones: 70 and 78 us for 1000
+// tokens; bands of 16 M tiles where A fits in L2: 2 to 3 % slower.
 // ---------------------------------------------------------------------------
 constexpr int kPairThreads = 320;
 constexpr int kPairMaxStages = 8;

@@ -331,11 +331,14 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
         uint16_t* yrow = args.y + static_cast<int64_t>(m0 + lane) * args.ldy;
         int acc = 0;
         uint32_t acc_phase = 0;
+        bool failed = false;      // a warp that gave up still meets the others at the barrier
         for (int nt = blockIdx.x; nt < args.n_tiles; nt += gridDim.x) {
             float* s_sw = s_scales + acc * kFewMaxBN;  // last read two tiles ago, before the previous barrier
             s_sw[tid] = nt * BN + tid < args.N && tid < BN ? args.sw[nt * BN + tid] : 0.0f;
             named_barrier_sync(1, 32 * kEpiWarps);
-            if (!mbar_wait_warp(&tmem_full[acc], acc_phase, args.timeout_ns, s_abort, args.status)) break;
+            if (!failed)
+                failed = !mbar_wait_warp(&tmem_full[acc], acc_phase, args.timeout_ns, s_abort, args.status);
+            if (failed) continue;
             tc_fence_after();
             // columns of the tile inside the matrix, in chunks of this warp
             const int cols = min(BN, args.N - nt * BN) - half * 16;

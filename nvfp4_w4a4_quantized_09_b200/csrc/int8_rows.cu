@@ -19,6 +19,24 @@
 // so the products that use it are NaN in that row and nowhere else.
 // r and the sum of squares are binary32; r is rounded to BF16 only where it is
 // stored, and the norm takes the unrounded value.
+//
+// Bound by memory: 7 bytes per element for the norm with a residual (2 + 2 read,
+// 2 + 1 written), 3 without and for the plain quantizer.  On a B200 (copies run
+// at 6.55 TB/s), CUDA-graph replay over rotating inputs:
+//   norm  32768 x 5120 182 us = 6.4 TB/s, 8192 x 5120 47.7 us = 6.2,
+//         16384 x 8192 148 us = 6.4, 8192 x 17408 193 us = 5.2 (one CTA of 96
+//         registers per SM), 4096 x 32768 204 us = 4.6 (staged in shared
+//         memory; 240 with a second pass over the row);
+//         without a residual 8192 x 5120 26 us = 4.8 (by then the instructions)
+//   plain 8191 x 17408 67.6 us = 6.3, 8192 x 5120 21.6 us = 5.8, 4096 x 32768
+//         62 us = 6.5
+//   one row of 5120 2.2 us, eight of 17408 2.1 us
+// What brought it there: one pass with the next row's loads in flight during
+// the reduction (norm 8192 x 5120: 70.6 us in two passes); the plain row held
+// in 16 bits and compared as 16-bit integers, so that two CTAs share an SM
+// (8191 x 17408: 77.3 us with binary32 held).  Packed f32x2 arithmetic was
+// slower (its register pairs spill: 61 us for norm 8192 x 5120), and its
+// multiplication is fused into the addition after it, which changes codes.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -4,6 +4,10 @@ add_rms_norm_int8 and int8_gemm against plain references.
 Codes, quantizer scales and GEMM outputs are compared bit for bit (their
 definitions leave one right value: binary32 steps and exact integer sums); the
 norm's scale within the bound that int8_reference.scale_tolerance derives."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -515,6 +519,34 @@ def test_a_captured_chain_replays_with_new_inputs(M):
         for got in outs:
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert nv.last_device_status() == 0
+
+
+FIRST_CALL = """
+import torch
+import nvfp4_w4a4_quantized_09_b200 as nv
+for M in (4, 300):
+    x = torch.randn(M, 512, device="cuda").bfloat16()
+    w = torch.ones(512, device="cuda").bfloat16()
+    W = nv.Int8Tensor(torch.randint(-127, 128, (256, 512), device="cuda", dtype=torch.int8),
+                      torch.rand(256, device="cuda"))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q, r = nv.add_rms_norm_int8(x, w, residual=x)
+        y = nv.int8_gemm(q, W)
+        c, s = nv.int8_quantize(x)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, nv.linear(nv.add_rms_norm_int8(x, w, residual=x)[0], W))
+    assert torch.equal(c, nv.int8_quantize(x)[0]) and nv.last_device_status() == 0
+"""
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True,
+                         timeout=300)
+    assert out.returncode == 0, out.stderr[-2000:]
 
 
 @pytest.mark.parametrize("M", [2, 140, 270])
