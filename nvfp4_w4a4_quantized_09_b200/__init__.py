@@ -12,6 +12,12 @@ W4A4 for the Recurrent Half of a Hybrid 27B LLM" -- NVFP4 (4-bit E2M1 elements,
 16 of them sharing one E4M3 scale) on weights and activations of every linear layer
 (evolve.pub review, Scope & Claims), served by fused multi-module GEMMs whose
 per-module global scales must be honoured (chatpaper.ai abstract).
+
+Beside it, the same layer in 8-bit integers (W8A8) for projections that keep
+eight bits: Int8Tensor weights and activations with one scale per row, made by
+int8_quantize_tensor or, together with the residual addition and RMS norm in
+front of a layer, by add_rms_norm_int8, and multiplied by int8_gemm; linear,
+mlp and the weight file take them too.
 """
 from __future__ import annotations
 
