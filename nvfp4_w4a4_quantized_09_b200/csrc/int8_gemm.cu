@@ -54,7 +54,8 @@ constexpr int kEpiWarps = 8;                    // two per TMEM lane quarter
 // and its BN / 2 rows of W per k-step of 128, the even CTA issues the MMAs
 // (M = 256, N = BN, K = 32), accumulator rows 0..127 live in the even CTA's
 // TMEM and 128..255 in the odd one's.  Two accumulators of 256 columns each:
-// the epilogue drains one while the MMAs fill the other.
+// the epilogue drains one while the MMAs fill the other -- or, with wide tiles
+// of 2 BN columns, both belong to one tile: A is loaded once for the two.
 //   warp 0      TMA producer (both CTAs; bytes counted on the even CTA's barrier)
 //   warp 1      MMA issuer (even CTA), TMEM owner
 //   warps 2..9  epilogue: two warps per TMEM lane quarter take alternate
@@ -65,9 +66,9 @@ constexpr int kEpiWarps = 8;                    // two per TMEM lane quarter
 // busy 97 % of the SMs' active time) and 955 to 1000 us back to back, where the
 // power limit holds the SMs at some 1.3 GHz.  Smaller products are bound by
 // shared memory, which the copies' writes and the MMAs' reads share, and by how
-// the tiles fill the rounds: 1000 x 5120 x 17408 (128 tiles of 160 columns on 74
-// pairs) 69 us, 512 x 24640 x 5120 48 us, 200 x 24640 x 5120 30 us, 517 x 2051 x
-// 1040 6.7 us.  Six stages of 32 KB against five: 1000 and 1062 us for the
+// the tiles fill the rounds: 1000 x 5120 x 17408 61 us, 1000 x 5120 x 5120 21.6
+// us, 512 x 24640 x 5120 48 us, 200 x 24640 x 5120 29 us, 517 x 2051 x 1040 6.7
+// us.  Six stages of 32 KB against five: 1000 and 1062 us for the
 // largest; spinning feed waits against suspending ones: 70 and 78 us for 1000
 // tokens; bands of 16 M tiles where A fits in L2: 2 to 3 % slower.
 // ---------------------------------------------------------------------------
@@ -89,20 +90,21 @@ struct PairArgs {
     int M, N, K;
     int m_tiles, n_tiles, k_steps;
     int group_m;                                // raster: m-tiles visited per n sweep
-    int bn;                                     // tile width
+    int bn;                                     // columns of an accumulator
+    int wide;                                   // 1: a tile fills both accumulators, 2 bn columns
     int stages;
     uint64_t timeout_ns;
     int* status;
 };
 
-__host__ __device__ constexpr uint32_t pair_stage_bytes(int bn) {
-    return static_cast<uint32_t>(kRows + bn / 2) * kStepBytes;
+__host__ __device__ constexpr uint32_t pair_stage_bytes(int bn, int wide) {
+    return static_cast<uint32_t>(kRows + ((bn / 2) << wide)) * kStepBytes;
 }
-__host__ __device__ constexpr int pair_stages(int bn) {
-    return static_cast<int>(kPairRing / pair_stage_bytes(bn)) < kPairMaxStages
-               ? static_cast<int>(kPairRing / pair_stage_bytes(bn)) : kPairMaxStages;
+__host__ __device__ constexpr int pair_stages(int bn, int wide) {
+    return static_cast<int>(kPairRing / pair_stage_bytes(bn, wide)) < kPairMaxStages
+               ? static_cast<int>(kPairRing / pair_stage_bytes(bn, wide)) : kPairMaxStages;
 }
-static_assert(pair_stages(256) >= 5, "the widest tile keeps a deep ring");
+static_assert(pair_stages(256, 0) >= 6 && pair_stages(256, 1) >= 4, "the widest tiles keep a deep ring");
 static_assert(kPairSmem > 228 * 1024 / 2, "two CTAs could share an SM and its 512 TMEM columns");
 
 __device__ __forceinline__ void pair_tile(int t, const PairArgs& a, int& mt, int& nt) {
@@ -126,7 +128,10 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
     const int STAGES = args.stages;
     const int BN = args.bn;
     constexpr uint32_t A_BYTES = kRows * kStepBytes;
-    const uint32_t B_BYTES = static_cast<uint32_t>(BN / 2) * kStepBytes;
+    const int wide = args.wide;
+    const int TN = BN << wide;                           // columns of a tile
+    const uint32_t HALF_B = static_cast<uint32_t>(BN / 2) * kStepBytes;   // this CTA's rows of BN
+    const uint32_t B_BYTES = HALF_B << wide;
     const uint32_t off_b = STAGES * A_BYTES;
     uint8_t* epi = smem + kPairRing;
     uint64_t* full = reinterpret_cast<uint64_t*>(epi + kPairEpi);
@@ -187,7 +192,9 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
         if (leader && once) {
             const int ahead = min(STAGES, args.k_steps);
             for (int kb = 0; kb < ahead; ++kb)
-                tma_prefetch_2d(&tmap_b, kb * kStepBytes, pair * BN + static_cast<int>(rank) * (BN / 2));
+                for (int h = 0; h <= wide; ++h)
+                    tma_prefetch_2d(&tmap_b, kb * kStepBytes,
+                                    pair * TN + h * BN + static_cast<int>(rank) * (BN / 2));
         }
         grid_dependency_wait();
         const uint64_t pol = l2_policy_evict_last();
@@ -200,7 +207,7 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             int mt, nt;
             pair_tile(t, args, mt, nt);
             const int ya = mt * 256 + static_cast<int>(rank) * kRows;
-            const int yb = nt * BN + static_cast<int>(rank) * (BN / 2);
+            const int yb = nt * TN + static_cast<int>(rank) * (BN / 2);
             for (int kb = 0; kb < args.k_steps; ++kb) {
                 if (!ready) failed |= !mbar_spin(empty0 + 8 * stage, phase ^ 1u, failed ? 1 : kSpinTries);
                 const int next = stage + 1 == STAGES ? 0 : stage + 1;
@@ -210,7 +217,9 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 if (leader && !failed) {
                     if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (A_BYTES + B_BYTES));
                     tma_load_2d_pair(smem + stage * A_BYTES, &tmap_a, fb, kb * kStepBytes, ya, pol);
-                    tma_load_2d_pair(smem + off_b + stage * B_BYTES, &tmap_b, fb, kb * kStepBytes, yb, pol_w);
+                    uint8_t* sb = smem + off_b + stage * B_BYTES;
+                    tma_load_2d_pair(sb, &tmap_b, fb, kb * kStepBytes, yb, pol_w);
+                    if (wide) tma_load_2d_pair(sb + HALF_B, &tmap_b, fb, kb * kStepBytes, yb + BN, pol_w);
                 }
                 __syncwarp();
                 if (rank == 0 && !failed) {
@@ -249,6 +258,7 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             bool failed = false, ready = false;
             for (int t = pair; t < total_tiles; t += npairs) {
                 failed |= !mbar_spin(acc_empty0 + 8 * acc, acc_phase ^ 1u, failed ? 1 : kSpinTries);
+                if (wide) failed |= !mbar_spin(acc_empty0 + 8, acc_phase ^ 1u, failed ? 1 : kSpinTries);
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * 256;
                 for (int kb = 0; kb < args.k_steps; ++kb) {
@@ -267,15 +277,30 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                             if (j < nmma)
                                 tc_mma_i8_pair(d_tmem, da + 2 * j, db + 2 * j, idesc,
                                                static_cast<uint32_t>(kb | j));
+                        if (wide) {
+                            const uint64_t db1 = db + (HALF_B >> 4);
+#pragma unroll
+                            for (int j = 0; j < kStepBytes / 32; ++j)
+                                if (j < nmma)
+                                    tc_mma_i8_pair(tmem_base + 256, da + 2 * j, db1 + 2 * j, idesc,
+                                                   static_cast<uint32_t>(kb | j));
+                        }
                         tc_commit_pair(&empty[stage], 0x3);
-                        if (kb == last_kb) tc_commit_pair(&tmem_full[acc], 0x3);
+                        if (kb == last_kb) {
+                            tc_commit_pair(&tmem_full[acc], 0x3);
+                            if (wide) tc_commit_pair(&tmem_full[1], 0x3);
+                        }
                     }
                     __syncwarp();
                     stage = next;
                     phase = next_phase;
                 }
-                acc ^= 1;
-                if (acc == 0) acc_phase ^= 1u;
+                if (wide) {                   // both accumulators, every tile
+                    acc_phase ^= 1u;
+                } else {
+                    acc ^= 1;
+                    if (acc == 0) acc_phase ^= 1u;
+                }
             }
             // every tcgen05 operation issued above has finished before TMEM is freed
             if (__any_sync(0xFFFFFFFFu, failed) && lane == 0) {
@@ -302,70 +327,78 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
         const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
         int acc = 0, buf = 0;
         uint32_t acc_phase = 0;
-        for (int t = pair; t < total_tiles; t += npairs) {
+        bool ok = true;
+        for (int t = pair; t < total_tiles && ok; t += npairs) {
             int mt, nt;
             pair_tile(t, args, mt, nt);
             const int m0 = mt * 256 + static_cast<int>(rank) * kRows + q * 32;   // row of lane 0
             const float sa = m0 + lane < args.M ? args.sa[m0 + lane] : 0.0f;
-            // the tile's channel scales are on their way while the MMAs run
-            float sw[kChunks];
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                const int c = half * 32 + 64 * i + lane;
-                sw[i] = m0 < args.M && c < BN && nt * BN + c < args.N ? args.sw[nt * BN + c] : 0.0f;
-            }
-            if (!mbar_wait_warp(&tmem_full[acc], acc_phase, args.timeout_ns, s_abort, args.status)) break;
-            tc_fence_after();
-            if (m0 < args.M) {                                         // warp-uniform
+            // an accumulator at a time: one a tile, or both of a wide one
+            for (int h = 0; h <= wide; ++h) {
+                const int nb = nt * TN + h * BN;
+                // its channels' scales are on their way while the MMAs run
+                float sw[kChunks];
 #pragma unroll
                 for (int i = 0; i < kChunks; ++i) {
-                    const int c = half * 32 + 64 * i;
-                    const int n0 = nt * BN + c;
-                    if (c >= BN || n0 >= args.N) break;                // warp-uniform
-                    uint32_t r[32];
-                    tmem_ld_32cols(tq + acc * 256 + c, r);
-                    tmem_ld_wait();
-                    uint32_t o[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        o[j] = scale_bf16x2(r[2 * j], r[2 * j + 1], sa, __shfl_sync(0xFFFFFFFFu, sw[i], 2 * j),
-                                            __shfl_sync(0xFFFFFFFFu, sw[i], 2 * j + 1));
-                    }
-                    if (n0 + 32 > args.N && (args.N & 7) != 0) {       // warp-uniform
-                        // TMA stores whole 16-byte pieces of a row: columns
-                        // that end inside one are stored from here
-                        if (m0 + lane < args.M) {
-                            uint16_t* yp = args.y + static_cast<int64_t>(m0 + lane) * args.ldy + n0;
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (n0 + j < args.N)
-                                    yp[j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
-                        }
-                        continue;
-                    }
-                    // the store that last used this buffer has finished reading it
-                    uint8_t* sb = stage_y + buf * kEpiBytes;
-                    const uint32_t sy = smem_u32(sb);
-                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                    __syncwarp();
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        sts128(sy + lane * 64 + ((static_cast<uint32_t>(u) ^ swz) << 4), o[4 * u],
-                               o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_2d(&tmap_y, sb, n0, m0, pol_y);
-                        bulk_commit_group();
-                    }
-                    buf ^= 1;
+                    const int c = half * 32 + 64 * i + lane;
+                    sw[i] = m0 < args.M && c < BN && nb + c < args.N ? args.sw[nb + c] : 0.0f;
                 }
+                if (!mbar_wait_warp(&tmem_full[acc], acc_phase, args.timeout_ns, s_abort, args.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (m0 < args.M) {                                         // warp-uniform
+#pragma unroll
+                    for (int i = 0; i < kChunks; ++i) {
+                        const int c = half * 32 + 64 * i;
+                        const int n0 = nb + c;
+                        if (c >= BN || n0 >= args.N) break;                // warp-uniform
+                        uint32_t r[32];
+                        tmem_ld_32cols(tq + acc * 256 + c, r);
+                        tmem_ld_wait();
+                        uint32_t o[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            o[j] = scale_bf16x2(r[2 * j], r[2 * j + 1], sa, __shfl_sync(0xFFFFFFFFu, sw[i], 2 * j),
+                                                __shfl_sync(0xFFFFFFFFu, sw[i], 2 * j + 1));
+                        }
+                        if (n0 + 32 > args.N && (args.N & 7) != 0) {       // warp-uniform
+                            // TMA stores whole 16-byte pieces of a row: columns
+                            // that end inside one are stored from here
+                            if (m0 + lane < args.M) {
+                                uint16_t* yp = args.y + static_cast<int64_t>(m0 + lane) * args.ldy + n0;
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    if (n0 + j < args.N)
+                                        yp[j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
+                            }
+                            continue;
+                        }
+                        // the store that last used this buffer has finished reading it
+                        uint8_t* sb = stage_y + buf * kEpiBytes;
+                        const uint32_t sy = smem_u32(sb);
+                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                        __syncwarp();
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            sts128(sy + lane * 64 + ((static_cast<uint32_t>(u) ^ swz) << 4), o[4 * u],
+                                   o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&tmap_y, sb, n0, m0, pol_y);
+                            bulk_commit_group();
+                        }
+                        buf ^= 1;
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster_relaxed(tmem_empty_leader + acc * 8);
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(tmem_empty_leader + acc * 8);
-            acc ^= 1;
-            if (acc == 0) acc_phase ^= 1u;
         }
         // every store of this warp has completed before the CTA exits
         if (lane == 0) bulk_wait_all();
@@ -547,19 +580,27 @@ nvfp4_status launch_pair(const Operands& o, const DeviceInfo& info, int* status,
     p.timeout_ns = kTimeoutNs;
     p.status = status;
     const int max_pairs = info.sms / 2;
-    // Tile width: a k-step of a tile costs the larger of its MMA time (2 BN
-    // cycles) and its feed ((128 + BN / 2) rows of 128 bytes at about 70 bytes
-    // per cycle and SM); take the width whose rounds of tiles cost least, the
-    // widest among equals.
+    // Tile width, by cycles of shared memory, which the copies' writes and the
+    // MMAs' reads share at 128 bytes a cycle: a k-step of BN columns writes 128 +
+    // BN / 2 rows of 128 bytes and reads 128 + BN; a wide one, of 2 BN columns,
+    // writes 128 + BN rows and reads twice 128 + BN, which is less than two
+    // narrow ones, but no MMAs overlap its epilogue (some 16 BN cycles an
+    // accumulator; of narrow tiles the last one's counts).  Take the width whose
+    // rounds of tiles cost least, the widest among equals.  (Measured for 1000 x
+    // 5120 x 17408, cycles a k-step: 393, 483, 519, 532 and 583 for BN = 128 to
+    // 256, against 448 to 640 by this rule; the product takes 61 us in wide tiles
+    // of 320 columns, one round, and 70 in narrow ones of 160, two rounds.)
     int64_t best = 0;
-    for (int bn = kPairMaxBN; bn >= 64; bn -= 32) {
-        const int64_t tiles = static_cast<int64_t>(p.m_tiles) * ((o.N + bn - 1) / bn);
-        const int64_t step = std::max(2 * bn, static_cast<int>(pair_stage_bytes(bn)) / 70);
-        const int64_t cost = (tiles + max_pairs - 1) / max_pairs * step;
-        if (best == 0 || cost < best) best = cost, p.bn = bn;
-    }
-    p.n_tiles = (o.N + p.bn - 1) / p.bn;
-    p.stages = pair_stages(p.bn);
+    for (int wide = 1; wide >= 0; --wide)
+        for (int bn = kPairMaxBN; bn >= (wide ? 160 : 64); bn -= 32) {
+            const int64_t tiles = static_cast<int64_t>(p.m_tiles) * ((o.N + (bn << wide) - 1) / (bn << wide));
+            const int64_t rounds = (tiles + max_pairs - 1) / max_pairs;
+            const int64_t cost = wide ? rounds * (p.k_steps * int64_t(384 + 3 * bn) + 32 * bn)
+                                      : rounds * p.k_steps * (256 + 3 * bn / 2) + 16 * bn;
+            if (best == 0 || cost < best) best = cost, p.bn = bn, p.wide = wide;
+        }
+    p.n_tiles = (o.N + (p.bn << p.wide) - 1) / (p.bn << p.wide);
+    p.stages = pair_stages(p.bn, p.wide);
     // Raster: when A fits comfortably in L2, sweep every M tile for each N tile
     // (the weight then streams from HBM once); otherwise bands of 16 M tiles.
     p.group_m = static_cast<int64_t>(o.M) * o.K <= (int64_t(48) << 20) ? 1 << 30 : 16;

@@ -310,7 +310,10 @@ def test_gemm_output_widths(M, N):
     (64, 5120, 1168), (16, 2048, 3200), (33, 151936, 128), (128, 40, 17408),
     # CTA pairs: every tile width, several rounds, bands of M tiles
     (200, 5120, 272), (300, 5120, 272), (200, 24640, 272), (520, 24640, 400), (257, 19000, 144),
-    (1000, 5120, 272), (2048, 5120, 144), (260, 151936, 64), (4200, 200, 13008)])
+    (1000, 5120, 272), (2048, 5120, 144), (260, 151936, 64), (4200, 200, 13008),
+    # ... and wide tiles, of both accumulators, N ending in either half
+    (1000, 5120, 2608), (200, 24635, 5136), (256, 34816, 4112), (130, 17003, 8192), (700, 4168, 8208),
+    (1000, 5120, 17408)])
 def test_gemm_configurations(M, N, K):
     a, w = gemm_inputs(M, N, K, seed=M + K)
     y = nv.int8_gemm(a, w)
