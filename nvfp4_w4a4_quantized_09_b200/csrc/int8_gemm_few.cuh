@@ -2,11 +2,11 @@
 // weight streams from memory once.  Included by int8_gemm.cu.
 //
 // One CTA per tile of all the tokens x BN channels, in one of two ways:
-//   * M > 32: the tokens are the MMA's 128 rows and the channels its N = BN, a
-//     multiple of 16 up to 256.  BN is free, so the launcher picks it to fill
+//   * M > 32: the tokens are the MMA's rows (64 of them up to 64 tokens, then
+//     128) and the channels its N = BN, a multiple of 16 up to 256.  BN is free, so the launcher picks it to fill
 //     whole rounds of the SMs: no split of K, no partial sums.  Only the
-//     tokens' own rows are loaded (NT = M rounded up to 8); the MMA reads 128
-//     rows from the tile's start, those beyond NT are whatever shared memory
+//     tokens' own rows are loaded (NT = M rounded up to 8); the MMA reads all
+//     its rows from the tile's start, those beyond NT are whatever shared memory
 //     holds there, and the accumulator lanes they fill are never read.
 //   * M <= 32 (kSwap): the channels are the MMA's 64 or 128 rows and the tokens
 //     its N = 16 or 32.  The same weight bytes then take an eighth to a quarter
@@ -212,7 +212,7 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
         // previous grid, however long it takes, has finished
         grid_dependency_wait();
         // D's rows are the tokens, or with kSwap the channels
-        const uint32_t idesc = kSwap ? int8_idesc(BN, args.nt) : int8_idesc(kRows, BN);
+        const uint32_t idesc = kSwap ? int8_idesc(BN, args.nt) : int8_idesc(args.nt <= 64 ? 64 : kRows, BN);
         const uint64_t da0 = sdesc_kmajor_sw128(smem_u32(kSwap ? smem + off_b : smem));
         const uint64_t db0 = sdesc_kmajor_sw128(smem_u32(kSwap ? smem : smem + off_b));
         const uint32_t da_step = (kSwap ? b_step : a_step) >> 4;
@@ -317,17 +317,20 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
         }
     } else {
         // ---------------- epilogue (warps 2..9) ----------------
-        // lane -> token; 16 channels at a time, a 32-byte sector of the row, the
-        // next chunk's TMEM load under way meanwhile.  The channels' scales pass
-        // through shared memory while the MMAs run.
+        // lane -> token (the first 16 lanes of a quarter where D has 64 rows); 16
+        // channels at a time, a 32-byte sector of the row, the next chunk's TMEM
+        // load under way meanwhile.  The channels' scales pass through shared
+        // memory while the MMAs run.
         constexpr int kChunks = kFewMaxBN / 32;       // per warp
         const int q = warp & 3;                       // TMEM lane quarter of this warp
         const int half = (warp - 2) >> 2;
-        const int m0 = q * 32;
-        const uint32_t tq = tmem_base + (static_cast<uint32_t>(m0) << 16) + half * 16;
+        const int per_q = args.nt <= 64 ? 16 : 32;
+        const int m0 = q * per_q;
+        const bool mine = lane < per_q && m0 + lane < args.M;
+        const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + half * 16;
         const int tid = threadIdx.x - 64;
         grid_dependency_wait();
-        const float sa = m0 + lane < args.M ? args.sa[m0 + lane] : 0.0f;
+        const float sa = mine ? args.sa[m0 + lane] : 0.0f;
         uint16_t* yrow = args.y + static_cast<int64_t>(m0 + lane) * args.ldy;
         int acc = 0;
         uint32_t acc_phase = 0;
@@ -359,7 +362,7 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     o[2 * j] = scale_bf16x2(r[i & 1][4 * j], r[i & 1][4 * j + 1], sa, w4.x, w4.y);
                     o[2 * j + 1] = scale_bf16x2(r[i & 1][4 * j + 2], r[i & 1][4 * j + 3], sa, w4.z, w4.w);
                 }
-                if (m0 + lane < args.M) {
+                if (mine) {
                     uint16_t* yp = yrow + n0;
                     if (n0 + 16 <= args.N) {
                         *reinterpret_cast<uint4*>(yp) = make_uint4(o[0], o[1], o[2], o[3]);
