@@ -523,7 +523,10 @@ nvfp4_status launch_few(const Operands& o, const DeviceInfo& info, int* status, 
     if (st != NVFP4_OK) return st;
     FewArgs f = {};
     f.sa = o.sa, f.sw = o.sw, f.y = o.y, f.ldy = o.ldy, f.M = o.M, f.N = o.N, f.K = o.K;
-    const bool swap = o.M <= kSwapTokens;
+    // Channels as the MMA's rows: a long stream of few tokens (see the top of
+    // int8_gemm_few.cuh), long enough for the power limit to show and to fill
+    // rounds of 128-channel tiles.
+    const bool swap = o.M <= kSwapTokens && o.N >= 224 * info.sms;
     f.nt = swap ? (o.M + 15) / 16 * 16 : (o.M + 7) / 8 * 8;
     f.k_steps = (o.K + kStepBytes - 1) / kStepBytes;
     f.timeout_ns = kTimeoutNs;
@@ -535,8 +538,8 @@ nvfp4_status launch_few(const Operands& o, const DeviceInfo& info, int* status, 
     // cycle.  The slower of the two decides; a quarter of the SMs' share is
     // added, so that among widths that memory bounds the least loaded SMs win,
     // and the last tile's epilogue (225 a chunk of a warp's 16 channels; swapped,
-    // it does not grow with the width).  Measured over 23 shapes, the choice is
-    // within 6 % of the best of all widths and stage depths.
+    // it does not grow with the width).  Measured over 20 shapes, the choice is
+    // within 4 % of the best of all widths and stage depths.
     int u = 0;
     int64_t best = 0;
     const int64_t memory = o.N * static_cast<int64_t>(kStepBytes) / 3400;

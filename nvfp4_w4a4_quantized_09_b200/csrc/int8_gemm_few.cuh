@@ -2,19 +2,21 @@
 // weight streams from memory once.  Included by int8_gemm.cu.
 //
 // One CTA per tile of all the tokens x BN channels, in one of two ways:
-//   * M > 32: the tokens are the MMA's rows (64 of them up to 64 tokens, then
-//     128) and the channels its N = BN, a multiple of 16 up to 256.  BN is free, so the launcher picks it to fill
-//     whole rounds of the SMs: no split of K, no partial sums.  Only the
-//     tokens' own rows are loaded (NT = M rounded up to 8); the MMA reads all
-//     its rows from the tile's start, those beyond NT are whatever shared memory
-//     holds there, and the accumulator lanes they fill are never read.
-//   * M <= 32 (kSwap): the channels are the MMA's 64 or 128 rows and the tokens
-//     its N = 16 or 32.  The same weight bytes then take an eighth to a quarter
-//     of the multiplications, and with them of the power: the first form drives
-//     the SM clock down to 1.5 GHz when such products run back to back (8 x
-//     34816 x 5120: 32.7 us in a long run against 27.7 in a short one; swapped
-//     28.1 and 27.5).  From some 40 tokens on the free BN gains more (64 x
-//     24640 x 5120: 24.1 us against 26.8 swapped, long runs).
+//   * The tokens are the MMA's rows (64 of them up to 64 tokens, then 128) and
+//     the channels its N = BN, a multiple of 16 up to 256.  BN is free, so the
+//     launcher picks it to fill whole rounds of the SMs: no split of K, no
+//     partial sums.  Only the tokens' own rows are loaded (NT = M rounded up to
+//     8); the MMA reads all its rows from the tile's start, those beyond NT are
+//     whatever shared memory holds there, and the accumulator lanes they fill
+//     are never read.
+//   * kSwap, for M <= 32 and 224 channels an SM or more: the channels are the
+//     MMA's 64 or 128 rows and the tokens its N = 16 or 32.  The same weight
+//     bytes then take a quarter to a half of the multiplications, and with them
+//     of the power, which in a long stream holds the SM clock down (8 x 34816 x
+//     5120 back to back: 28.0 us swapped, 29.0 not; 8 x 151936 x 5120: 117 and
+//     124; in short runs 27.4 and 26.9, 115 and 116).  With fewer channels the
+//     fixed tile heights fill the rounds worse (32 x 24640 x 5120: 22.4 us
+//     swapped, 21.4 not; 1 x 5120 x 5120: 8.5 and 7.3).
 // Common to both:
 //   * A pipeline stage holds U = 1, 2, 4 or 8 steps of 128 values of K, the
 //     most that 58 KB take: each stage costs the MMA warp a handshake during
@@ -24,11 +26,11 @@
 //     memory first waits for the previous grid (griddepcontrol.wait); the
 //     first ring of weights is prefetched into L2 before that (5 to 7 % of a
 //     call, measured for 24640 and 34816 channels).
-// Bound by memory: 8 x 34816 x 5120 27.5 us = 6.5 TB/s, 1 x 24640 x 5120 21.0 us
-// = 6.0 TB/s, 100 x 24640 x 5120 22.4 us = 5.9 TB/s, 8 x 151936 x 5120 115 us =
-// 6.8 TB/s (CUDA-graph replay).  Small products are bound by what a launch
-// costs around its stream: 16 x 2048 x 2048 4.2 us, 1 x 5120 x 5120 8.2 us for
-// 26 MB.
+// Bound by memory: 8 x 34816 x 5120 27.4 us = 6.5 TB/s, 1 x 24640 x 5120 20.0 us
+// = 6.3 TB/s, 100 x 24640 x 5120 22.4 us = 5.9 TB/s, 1 x 5120 x 17408 16.7 us =
+// 5.3 TB/s, 8 x 151936 x 5120 115 us = 6.8 TB/s (CUDA-graph replay).  Small
+// products are bound by what a launch costs around its stream: 16 x 2048 x 2048
+// 3.6 us, 1 x 5120 x 5120 7.2 us for 26 MB.
 //
 // Roles (10 warps): 0 TMA producer; 1 TMEM owner and MMA issuer; 2..9 epilogue,
 // two warps per TMEM lane quarter on alternate 16-column chunks.  Every wait is
