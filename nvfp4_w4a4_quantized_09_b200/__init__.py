@@ -484,7 +484,7 @@ def silu_mul(gate_up: torch.Tensor, h: Optional[torch.Tensor] = None, stream=Non
         _check_out_matrix(h, "h", torch.bfloat16, rows, f)
     dev = _check_devices(gate_up=gate_up, h=h)
     if h is None:
-        h = torch.empty(rows, f, dtype=torch.bfloat16, device=dev)
+        h = _empty(rows, f, dtype=torch.bfloat16, device=dev, stream=stream)
     _lib.check("nvfp4_silu_mul", _lib.lib().nvfp4_silu_mul(
         _ptr(gate_up), rows, f, gate_up.stride(0), _ptr(h), h.stride(0), _stream(stream)))
     return h
@@ -522,7 +522,7 @@ def gemm_silu_mul(a: QuantizedTensor, w_interleaved: QuantizedTensor,
     dev = _check_devices(a_codes=a.codes, a_sf=a.sf, a_g=a.g, w_codes=w_interleaved.codes,
                          w_sf=w_interleaved.sf, w_g=w_interleaved.g, h=h)
     if h is None:
-        h = torch.empty(M, F, dtype=torch.bfloat16, device=dev)
+        h = _empty(M, F, dtype=torch.bfloat16, device=dev, stream=stream)
     g_h = torch.empty(1, dtype=torch.float32, device=dev)
     amax_h = torch.empty(1, dtype=torch.float32, device=dev)
     _lib.check("nvfp4_gemm_silu_mul", _lib.lib().nvfp4_gemm_silu_mul(
@@ -548,6 +548,8 @@ def mlp(x: torch.Tensor, w_gate_up, w_down, stream=None, interleaved: bool = Fal
     if not isinstance(w_gate_up, QuantizedTensor):
         raise TypeError("the interleaved gate_up weight must be a QuantizedTensor")
     h, g_h, _ = gemm_silu_mul(quantize_tensor(x, stream=stream), w_gate_up, stream=stream)
+    if isinstance(w_down, Int8Tensor):
+        return linear(h, w_down, stream=stream)
     codes, sf = quantize(h, g_h, stream=stream)
     return gemm(QuantizedTensor(codes, sf, g_h, h.shape[0], h.shape[1]), w_down, stream=stream)
 

@@ -487,6 +487,39 @@ def test_mlp_mixes_4_and_8_bits():
     assert torch.equal(y, want)
 
 
+def test_mlp_with_an_interleaved_gate_up_takes_an_8_bit_down_projection():
+    x = activations(300, 256, seed=1)                # the fused gate_up is for more than 256 tokens
+    gate_up = synth.gaussian_weights(512, 256, 0.05, seed=2, device=DEV)
+    w4 = nv.quantize_tensor(nv.interleave_gate_up(gate_up))
+    w8 = nv.int8_quantize_tensor(synth.gaussian_weights(256, 256, 0.05, seed=3, device=DEV))
+    y = nv.mlp(x, w4, w8, interleaved=True)
+    h, _, _ = nv.gemm_silu_mul(nv.quantize_tensor(x), w4)
+    torch.cuda.synchronize()
+    assert same(f32(y), ref.gemm(*ref.quantize(f32(h)), w8.codes.cpu().numpy(), f32(w8.scale)))
+
+
+@pytest.mark.parametrize("M", [4, 300])
+def test_mlp_on_another_stream_keeps_its_intermediates(M):
+    # nothing that the call allocated and dropped may be handed out again on
+    # the caller's stream while the other one still works on it
+    H, I = 256, 512
+    x = activations(M, H, seed=1)
+    w1 = nv.int8_quantize_tensor(synth.gaussian_weights(2 * I, H, 0.05, seed=2, device=DEV))
+    w2 = nv.int8_quantize_tensor(synth.gaussian_weights(H, I, 0.05, seed=3, device=DEV))
+    want = nv.mlp(x, w1, w2)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(100_000_000)           # some 50 ms
+        got = nv.mlp(x, w1, w2, stream=s)
+        fill = [torch.full(shape, 0x7F, dtype=torch.int8, device=DEV)
+                for shape in ((M, 2 * H), (M, 2 * I), (M, 4 * I), (M, H), (M, I), (4 * M,)) for _ in range(2)]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        del fill
+
+
 @pytest.mark.parametrize("M", [4, 300])
 def test_a_captured_chain_replays_with_new_inputs(M):
     H = 1024
