@@ -504,20 +504,31 @@ void launch_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2], int 
 
 nvfp4_status launch_few(const Operands& o, const DeviceInfo& info, int* status, cudaStream_t stream) {
     using Kernel = void (*)(CUtensorMap, CUtensorMap, FewArgs);
-    static const Kernel kernels[2][4] = {
-        {int8_gemm_few_kernel<1, false>, int8_gemm_few_kernel<2, false>, int8_gemm_few_kernel<4, false>,
-         int8_gemm_few_kernel<8, false>},
-        {int8_gemm_few_kernel<1, true>, int8_gemm_few_kernel<2, true>, int8_gemm_few_kernel<4, true>,
-         int8_gemm_few_kernel<8, true>}};
+    static const Kernel kernels[3][4] = {
+        {int8_gemm_few_kernel<1, false, false>, int8_gemm_few_kernel<2, false, false>,
+         int8_gemm_few_kernel<4, false, false>, int8_gemm_few_kernel<8, false, false>},
+        {int8_gemm_few_kernel<1, true, false>, int8_gemm_few_kernel<2, true, false>,
+         int8_gemm_few_kernel<4, true, false>, int8_gemm_few_kernel<8, true, false>},
+        {int8_gemm_few_kernel<1, false, true>, int8_gemm_few_kernel<2, false, true>,
+         int8_gemm_few_kernel<4, false, true>, int8_gemm_few_kernel<8, false, true>}};
     static PerDeviceOnce once;
+    static int resident[kMaxDevices][kMaxSplits + 1];     // clusters of 2, 4 and 8 CTAs that fit the device
     int dev = 0;
     nvfp4_status st = current_device(&dev);
     if (st != NVFP4_OK) return st;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
     st = once.run(dev, [&] {
         for (const auto& row : kernels)
             for (const Kernel k : row)
                 if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem) != cudaSuccess)
                     return NVFP4_ERR_CUDA;
+        for (int s = 2; s <= kMaxSplits; s *= 2) {
+            launch_config(&cfg, attr, s, kFewThreads, kFewSmem, nullptr);
+            cfg.gridDim = dim3(static_cast<unsigned>(info.sms / s * s), 1, 1);
+            if (cudaOccupancyMaxActiveClusters(&resident[dev][s], kernels[2][0], &cfg) != cudaSuccess)
+                return NVFP4_ERR_CUDA;
+        }
         return NVFP4_OK;
     });
     if (st != NVFP4_OK) return st;
@@ -531,37 +542,44 @@ nvfp4_status launch_few(const Operands& o, const DeviceInfo& info, int* status, 
     f.k_steps = (o.K + kStepBytes - 1) / kStepBytes;
     f.timeout_ns = kTimeoutNs;
     f.status = status;
-    // Tile width, by cycles.  Over all rounds of tiles an SM spends on each
-    // k-step the larger of its MMAs (four of BN / 2, 52 at the least, and 230
-    // for a stage's handshake) and its feed (about 42 bytes a cycle while all
-    // SMs stream); memory as a whole delivers some 3400 bytes of weights a
-    // cycle.  The slower of the two decides; a quarter of the SMs' share is
-    // added, so that among widths that memory bounds the least loaded SMs win,
-    // and the last tile's epilogue (225 a chunk of a warp's 16 channels; swapped,
-    // it does not grow with the width).  Measured over 20 shapes, the choice is
-    // within 4 % of the best of all widths and stage depths.
+    // Tile width and the split of K, by cycles.  Over all rounds of tiles an SM
+    // spends on each k-step the larger of its MMAs (four of BN / 2, 56 at the
+    // least or 44 with 64 rows, and 300 for a stage's handshake) and its feed
+    // (48 bytes a cycle); memory as a whole delivers some 3400 bytes of weights
+    // a cycle.  The slower of the two decides; a quarter of the SMs' share is
+    // added, so that among widths that memory bounds the least loaded SMs win.
+    // Sharing K among the CTAs of a cluster costs 3500 and the exchange of the
+    // sums, 10 bytes a cycle.  Measured for 90 shapes of up to 128 tokens, the
+    // choice takes 1 % longer than the best of all widths and splits on average.
     int u = 0;
     int64_t best = 0;
     const int64_t memory = o.N * static_cast<int64_t>(kStepBytes) / 3400;
-    for (int bn = swap ? 64 : 16; bn <= (swap ? 128 : kFewMaxBN); bn += swap ? 64 : 16) {
-        const int64_t tiles = (o.N + bn - 1) / bn;
-        int bu = 0, bs = 0;
-        few_config(f.nt, bn, &bu, &bs);
-        const int64_t sm = (tiles + info.sms - 1) / info.sms *
-                           std::max(4 * std::max(52, bn / 2) + 230 / bu, (f.nt + bn) * kStepBytes / 42);
-        const int64_t cost = f.k_steps * (std::max(sm, memory) + sm / 4) + (swap ? 0 : (bn + 31) / 32 * 225);
-        if (best == 0 || cost < best) best = cost, f.bn = bn, f.stages = bs, u = bu;
+    const int max_splits = swap ? 1 : kMaxSplits;
+    for (int splits = 1; splits <= max_splits; splits *= 2) {
+        const int unit = swap ? 64 : 16 * splits, fit = splits == 1 ? info.sms : resident[dev][splits];
+        if (fit <= 0) continue;
+        for (int bn = unit; bn <= (swap ? 128 : kFewMaxBN); bn += unit) {
+            const int64_t tiles = (o.N + bn - 1) / bn;
+            int bu = 0, bs = 0;
+            few_config(f.nt, bn, &bu, &bs);
+            if (splits > 1 && f.k_steps < bu * splits) continue;       // a stage for every CTA
+            const int64_t step = std::max(4 * std::max(f.nt <= 64 ? 44 : 56, bn / 2) + 300 / bu,
+                                          (f.nt + bn) * kStepBytes / 48);
+            const int64_t sm = (tiles + fit - 1) / fit * step / splits;
+            const int64_t cost = f.k_steps * (std::max(sm, memory) + sm / 4) +
+                                 (splits > 1 ? 3500 + f.nt * bn * 4 * (splits - 1) / splits / 10 : 0);
+            if (best == 0 || cost < best) best = cost, f.bn = bn, f.stages = bs, f.splits = splits, u = bu;
+        }
     }
     f.n_tiles = (o.N + f.bn - 1) / f.bn;
-    const Kernel kern = kernels[swap][u == 8 ? 3 : u / 2];
+    const Kernel kern = kernels[swap ? 1 : f.splits > 1 ? 2 : 0][u == 8 ? 3 : u / 2];
     CUtensorMap ta, tw;
     f.wide = o.K % kStepBytes == 0;
     if (!make_steps_map(&ta, o.a, o.M, o.K, f.nt, u) || !make_steps_map(&tw, o.w, o.N, o.K, f.bn, u))
         return NVFP4_ERR_CUDA;
-    cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr[2];
-    launch_config(&cfg, attr, 1, kFewThreads, kFewSmem, stream);
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min(f.n_tiles, info.sms)), 1, 1);
+    launch_config(&cfg, attr, f.splits, kFewThreads, kFewSmem, stream);
+    cfg.gridDim = dim3(static_cast<unsigned>(f.splits > 1 ? f.n_tiles * f.splits : std::min(f.n_tiles, info.sms)), 1,
+                       1);
     if (cudaLaunchKernelEx(&cfg, kern, ta, tw, f) != cudaSuccess) return NVFP4_ERR_CUDA;
     return cuda_status(cudaGetLastError());
 }

@@ -1,11 +1,10 @@
 // int8_gemm_few.cuh -- the int8 GEMM for few tokens (M <= 128), where the
 // weight streams from memory once.  Included by int8_gemm.cu.
 //
-// One CTA per tile of all the tokens x BN channels, in one of two ways:
+// Tiles of all the tokens x BN channels, in one of three ways:
 //   * The tokens are the MMA's rows (64 of them up to 64 tokens, then 128) and
 //     the channels its N = BN, a multiple of 16 up to 256.  BN is free, so the
-//     launcher picks it to fill whole rounds of the SMs: no split of K, no
-//     partial sums.  Only the tokens' own rows are loaded (NT = M rounded up to
+//     launcher picks it to fill whole rounds of the SMs.  Only the tokens' own rows are loaded (NT = M rounded up to
 //     8); the MMA reads all its rows from the tile's start, those beyond NT are
 //     whatever shared memory holds there, and the accumulator lanes they fill
 //     are never read.
@@ -17,6 +16,15 @@
 //     124; in short runs 27.4 and 26.9, 115 and 116).  With fewer channels the
 //     fixed tile heights fill the rounds worse (32 x 24640 x 5120: 22.4 us
 //     swapped, 21.4 not; 1 x 5120 x 5120: 8.5 and 7.3).
+//   * kSplit, where the tiles are few or narrow and K is long: a cluster of 2, 4
+//     or 8 CTAs shares a tile's K, and each of them then owns a slice of the
+//     tile's columns, to which the others' sums come through distributed shared
+//     memory.  A narrow tile spends its time bringing the tokens in again (they
+//     weigh more than its channels) at a rate that one SM bounds; wider tiles
+//     with a part of K each bring in less.  The exchange costs 2 us and more:
+//     100 x 5120 x 17408 19.7 us, 27.0 by whole tiles; 128 x 2048 x 17408 12.0
+//     and 24.8; 16 x 2048 x 17408 9.5 and 13.3; 1 x 256 x 17408 6.9 and 12.3;
+//     but 64 x 5120 x 5120 8.4 and 8.0, which stays whole.
 // Common to both:
 //   * A pipeline stage holds U = 1, 2, 4 or 8 steps of 128 values of K, the
 //     most that 58 KB take: each stage costs the MMA warp a handshake during
@@ -41,6 +49,7 @@ constexpr int kFewMaxTokens = 128;
 constexpr int kSwapTokens = 32;                      // at most: channels as the MMA's rows
 constexpr int kFewMaxStages = 16;
 constexpr int kFewMaxBN = 256;
+constexpr int kMaxSplits = 8;                        // CTAs of a cluster that share a tile's K
 constexpr uint32_t kFewSmem = 227 * 1024;            // whole: one CTA per SM
 constexpr uint32_t kFewBars = (2 * kFewMaxStages + 5) * 8;
 constexpr uint32_t kFewScales = 2 * kFewMaxBN * 4;    // channel scales, one set per accumulator
@@ -57,6 +66,7 @@ struct FewArgs {
     int bn;          // channels per tile
     int wide;        // one copy brings a stage's U steps of an operand
     int stages;
+    int splits;      // CTAs of a cluster that share a tile's K
     uint64_t timeout_ns;
     int* status;
 };
@@ -86,7 +96,7 @@ constexpr bool few_configs_fit() {
 static_assert(few_configs_fit(), "a few-token configuration does not fit");
 static_assert(kFewSmem > 228 * 1024 / 2, "two CTAs could share an SM and its 512 TMEM columns");
 
-template <int U, bool kSwap>
+template <int U, bool kSwap, bool kSplit>
 __global__ void __launch_bounds__(kFewThreads, 1)
 int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
                      const __grid_constant__ CUtensorMap tmap_w, const FewArgs args) {
@@ -109,6 +119,12 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int k_stages = (args.k_steps + U - 1) / U;     // stages per tile
+    // this CTA's tiles and its stages of each: all, or its part of one tile's
+    const int rank = kSplit ? static_cast<int>(cluster_ctarank()) : 0;
+    const int first = kSplit ? static_cast<int>(blockIdx.x) / args.splits : static_cast<int>(blockIdx.x);
+    const int stride = kSplit ? args.n_tiles : static_cast<int>(gridDim.x);
+    const int ks0 = kSplit ? rank * k_stages / args.splits : 0;
+    const int ks1 = kSplit ? (rank + 1) * k_stages / args.splits : k_stages;
     grid_launch_dependents();
 
     if (warp == 0) {
@@ -150,9 +166,9 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
         // While the previous grid finishes, the first ring of weights moves
         // into L2 (a hint: nothing of it is read before the wait).
         if (leader && args.wide) {
-            const int ahead = min(STAGES, k_stages);
-            for (int ks = 0; ks < ahead; ++ks)
-                tma_prefetch_3d(&tmap_w, 0, static_cast<int>(blockIdx.x) * BN, ks * U);
+            const int ahead = min(ks0 + STAGES, ks1);
+            for (int ks = ks0; ks < ahead; ++ks)
+                tma_prefetch_3d(&tmap_w, 0, first * BN, ks * U);
         }
         grid_dependency_wait();
         const uint64_t pol_w = l2_policy_evict_first();   // each weight byte is read once
@@ -162,8 +178,8 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
         int stage = 0;
         uint32_t phase = 0;
         bool ready = true;                                // the ring starts empty
-        for (int nt = blockIdx.x; nt < args.n_tiles; nt += gridDim.x) {
-            for (int ks = 0; ks < k_stages; ++ks) {
+        for (int nt = first; nt < args.n_tiles; nt += stride) {
+            for (int ks = ks0; ks < ks1; ++ks) {
                 if (!ready) failed |= !mbar_spin(empty0 + 8 * stage, phase ^ 1u, failed ? 1 : kSpinTries);
                 const int next = stage + 1 == STAGES ? 0 : stage + 1;
                 const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
@@ -225,11 +241,11 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
         int stage = 0, acc = 0;
         uint32_t phase = 0, acc_phase = 0;
         bool ready = false;
-        for (int nt = blockIdx.x; nt < args.n_tiles; nt += gridDim.x) {
+        for (int nt = first; nt < args.n_tiles; nt += stride) {
             failed |= !mbar_spin(acc_empty0 + 8 * acc, acc_phase ^ 1u, failed ? 1 : kSpinTries);
             tc_fence_after();
             const uint32_t d_tmem = tmem_base + acc * 256;
-            for (int ks = 0; ks < k_stages; ++ks) {
+            for (int ks = ks0; ks < ks1; ++ks) {
                 if (!ready) failed |= !mbar_spin(full0 + 8 * stage, phase, failed ? 1 : kSpinTries);
                 tc_fence_after();
                 const int next = stage + 1 == STAGES ? 0 : stage + 1;
@@ -245,17 +261,17 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
 #pragma unroll
                             for (int j = 0; j < kStepBytes / 32; ++j)
                                 tc_mma_i8(d_tmem, da + i * da_step + 2 * j, db + i * db_step + 2 * j, idesc,
-                                          static_cast<uint32_t>(ks | i | j));
+                                          static_cast<uint32_t>((ks - ks0) | i | j));
                     } else {
                         // the last stage ends with K
                         for (int i = 0; i < last_n; ++i) {
                             const uint32_t j = 2 * (i & 3);
                             tc_mma_i8(d_tmem, da + (i >> 2) * da_step + j, db + (i >> 2) * db_step + j, idesc,
-                                      static_cast<uint32_t>(ks | i));
+                                      static_cast<uint32_t>((ks - ks0) | i));
                         }
                     }
                     tc_commit(&empty[stage]);
-                    if (ks == k_stages - 1) tc_commit(&tmem_full[acc]);
+                    if (ks == ks1 - 1) tc_commit(&tmem_full[acc]);
                 }
                 __syncwarp();
                 stage = next;
@@ -291,7 +307,7 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
         named_barrier_sync(1, 32 * kEpiWarps);
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (int nt = blockIdx.x; nt < args.n_tiles; nt += gridDim.x) {
+        for (int nt = first; nt < args.n_tiles; nt += stride) {
             const int n = nt * BN + q * per_q + lane;
             const bool mine = lane < per_q && n < args.N;
             const float sw = mine ? args.sw[n] : 0.0f;      // on its way while the MMAs run
@@ -317,6 +333,13 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
         }
+    } else if constexpr (kSplit) {
+        // ---------------- epilogue (warps 2..9): this CTA's sums are complete ----------------
+        const int tid = threadIdx.x - 64, n = first * BN + tid;
+        grid_dependency_wait();
+        s_scales[tid] = tid < BN && n < args.N ? args.sw[n] : 0.0f;
+        mbar_wait_warp(&tmem_full[0], 0, args.timeout_ns, s_abort, args.status);
+        __syncwarp();
     } else {
         // ---------------- epilogue (warps 2..9) ----------------
         // lane -> token (the first 16 lanes of a quarter where D has 64 rows); 16
@@ -337,7 +360,7 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
         int acc = 0;
         uint32_t acc_phase = 0;
         bool failed = false;      // a warp that gave up still meets the others at the barrier
-        for (int nt = blockIdx.x; nt < args.n_tiles; nt += gridDim.x) {
+        for (int nt = first; nt < args.n_tiles; nt += stride) {
             float* s_sw = s_scales + acc * kFewMaxBN;  // last read two tiles ago, before the previous barrier
             s_sw[tid] = nt * BN + tid < args.N && tid < BN ? args.sw[nt * BN + tid] : 0.0f;
             named_barrier_sync(1, 32 * kEpiWarps);
@@ -382,6 +405,79 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
         }
+    }
+
+    if constexpr (kSplit) {
+        // The CTAs of the cluster own a slice of the tile's columns each.  Every
+        // CTA stores its sums of the other slices into their owners' shared
+        // memory, where the ring has served; the owner adds them to its own.
+        // Integers: the order is free.  Lanes are tokens, 16 bytes of a token
+        // apart by 16 bytes: a warp's store is 512 consecutive bytes.
+        cluster_sync();                                  // every ring has been read
+        tc_fence_after();
+        const int q = warp & 3, half = (warp - 2) >> 2;
+        const int per_q = args.nt <= 64 ? 16 : 32;
+        const int m = q * per_q + lane;
+        const bool warp_mine = warp >= 2 && q * per_q < args.M;
+        const bool mine = warp_mine && lane < per_q && m < args.M;
+        const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+        const int slice = BN / 16 / args.splits;         // chunks of 16 columns
+        const int chunks = min(BN, args.N - first * BN + 15) / 16;
+        const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(m) * 16;
+        constexpr uint32_t kUnit = kRows * 16;           // 4 columns of all tokens
+        if (warp_mine) {
+            for (int c = half; c < chunks; c += 2) {
+                const int owner = c / slice;
+                if (owner == rank) continue;
+                uint32_t r[16];
+                tmem_ld_16cols(tq + 16 * c, r);
+                tmem_ld_wait();
+                const int slot = (rank - (rank > owner)) * slice + c - owner * slice;
+                const uint32_t to = mapa_shared(ring, owner) + static_cast<uint32_t>(slot) * 4 * kUnit;
+                if (mine)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        st_cluster_v4(to + g * kUnit, r[4 * g], r[4 * g + 1], r[4 * g + 2], r[4 * g + 3]);
+                __syncwarp();
+            }
+        }
+        __syncwarp();
+        cluster_sync();                                  // every sum has arrived
+        if (warp_mine) {
+            const float sa = mine ? args.sa[m] : 0.0f;
+            const int end = min(chunks, (rank + 1) * slice);
+            for (int c = rank * slice + half; c < end; c += 2) {
+                uint32_t r[16];
+                tmem_ld_16cols(tq + 16 * c, r);
+                tmem_ld_wait();
+                if (mine) {
+                    uint32_t from = ring + static_cast<uint32_t>(c - rank * slice) * 4 * kUnit;
+                    for (int i = 1; i < args.splits; ++i, from += static_cast<uint32_t>(slice) * 4 * kUnit)
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const uint4 v = lds128(from + g * kUnit);
+                            r[4 * g] += v.x, r[4 * g + 1] += v.y, r[4 * g + 2] += v.z, r[4 * g + 3] += v.w;
+                        }
+                    uint32_t o[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        o[j] = scale_bf16x2(r[2 * j], r[2 * j + 1], sa, s_scales[16 * c + 2 * j],
+                                            s_scales[16 * c + 2 * j + 1]);
+                    const int n0 = first * BN + 16 * c;
+                    uint16_t* yp = args.y + static_cast<int64_t>(m) * args.ldy + n0;
+                    if (n0 + 16 <= args.N) {
+                        *reinterpret_cast<uint4*>(yp) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4*>(yp + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (n0 + j < args.N) yp[j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        __syncwarp();
     }
 
     tc_fence_before();

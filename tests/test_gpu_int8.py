@@ -325,6 +325,45 @@ def test_gemm_configurations(M, N, K):
     assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("M,N,K", [
+    # narrow products of long rows, where the CTAs of a cluster share K: two,
+    # four and eight of them, parts of unequal length, N and K that end inside
+    # a chunk, a slice, a step and an instruction, M of 1 to 128 MMA rows
+    (1, 256, 17408), (3, 169, 27056), (7, 300, 8192), (16, 80, 131056), (20, 6819, 10864), (33, 1024, 28672),
+    (34, 1, 10128), (55, 579, 13600), (64, 2051, 8208), (64, 5120, 17408), (65, 80, 22080), (65, 1000, 5136),
+    (97, 6738, 19776), (100, 5120, 17408), (104, 4867, 25488), (114, 1111, 2544), (121, 517, 17424),
+    (128, 2048, 17408), (128, 8, 131056), (128, 8192, 17408)])
+def test_gemm_shares_long_rows_among_ctas(M, N, K):
+    a, w = gemm_inputs(M, N, K, seed=M + K)
+    y = torch.full((M, (N + 23) // 8 * 8), 7.0, dtype=BF, device=DEV)
+    for _ in range(3):
+        nv.int8_gemm(a, w, y[:, :N])
+    torch.cuda.synchronize()
+    assert nv.last_device_status() == 0
+    acc = a.codes.double() @ w.codes.double().t()        # exact
+    assert torch.equal(y[:, :N], (acc.float() * a.scale[:, None] * w.scale[None, :]).to(BF))
+    assert bool((y[:, N:] == 7).all())
+
+
+def test_gemm_shared_rows_on_two_streams_and_captured():
+    a, w = gemm_inputs(100, 2048, 17408, seed=1)
+    b, v = gemm_inputs(40, 300, 28672, seed=2)
+    want = nv.int8_gemm(a, w), nv.int8_gemm(b, v)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [(nv.int8_gemm(a, w, stream=s), nv.int8_gemm(b, v, stream=s)) for _ in range(10) for s in streams]
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        for _ in range(4):
+            got.append((nv.int8_gemm(a, w), nv.int8_gemm(b, v)))
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert nv.last_device_status() == 0
+    assert all(torch.equal(x, want[0]) and torch.equal(y, want[1]) for x, y in got)
+
+
 @pytest.mark.parametrize("M", [1, 5, 129, 300])
 @pytest.mark.parametrize("fill", [(-128, -128), (127, -128), (127, 127)])
 def test_gemm_largest_sums(M, fill):
