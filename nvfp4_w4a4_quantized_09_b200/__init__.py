@@ -760,9 +760,12 @@ def int8_gemm(a: Int8Tensor, w: Int8Tensor, y: Optional[torch.Tensor] = None,
         _check_devices(a_codes=ac, a_scale=asc, w_codes=wc, w_scale=wsc, y=y)
     ldy = (N + 7) // 8 * 8
     if y is None:
-        y = _empty(M, ldy, dtype=_BF16, device=ac.device, stream=stream)
-        if ldy != N:
-            y = y[:, :N]
+        if ldy == N:
+            y = _empty(M, N, dtype=_BF16, device=ac.device, stream=stream)
+        elif stream is None:             # rows padded, in one call
+            y = torch.empty_strided((M, N), (ldy, 1), dtype=_BF16, device=ac.device)
+        else:
+            y = _empty(M, ldy, dtype=_BF16, device=ac.device, stream=stream)[:, :N]
     elif M > 1:
         ldy = y.stride(0)
     st = _lib.lib().nvfp4_int8_gemm(ac.data_ptr(), asc.data_ptr(), wc.data_ptr(), wsc.data_ptr(),

@@ -44,6 +44,89 @@ __device__ __forceinline__ uint32_t scale_bf16x2(uint32_t acc0, uint32_t acc1, f
 }
 
 constexpr int kEpiWarps = 8;                    // two per TMEM lane quarter
+constexpr int kMaxSplits = 8;                   // CTAs of a cluster that share a tile's K
+
+// A tile whose K the CTAs of a cluster share: `splits` of them (in the pair
+// kernel pairs of them) hold sums of 128 rows x 16 * slice * splits columns in
+// TMEM, and number r owns the r-th slice.
+struct Slices {
+    int splits, rank;
+    int step, offset;                           // owner r is CTA step * r + offset of the cluster
+    int slice;                                  // chunks of 16 columns each owns
+    int chunks;                                 // of the tile inside the matrix
+};
+
+// By all threads of every CTA of the cluster, once its sums are complete.  Every
+// CTA stores its sums of the other slices into their owners' shared memory,
+// where the ring (at `ring`) has served; the owner adds them to its own and
+// stores the product.  Integers: the order is free.  A lane is a row (`m` of the
+// tile, `row` of the matrix; `per_q` of a warp's lanes are in use), 4 columns of
+// consecutive rows are consecutive 16 bytes.
+__device__ __forceinline__ void exchange_and_store(const Slices& sl, uint32_t tmem_base, uint32_t ring,
+                                                   const float* s_sw, const float* gsa, uint16_t* y, int64_t ldy,
+                                                   int m, int row, int M, int per_q, int n_base, int N) {
+    constexpr uint32_t kUnit = kRows * 16;      // 4 columns of all rows
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int half = (warp - 2) >> 2;
+    const bool warp_mine = warp >= 2 && row - lane < M;
+    const bool mine = warp_mine && lane < per_q && row < M;
+    const uint32_t tq = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    ring += static_cast<uint32_t>(m) * 16;
+    cluster_sync();                             // every ring has been read
+    tc_fence_after();
+    if (warp_mine) {
+        for (int c = half; c < sl.chunks; c += 2) {
+            const int owner = c / sl.slice;
+            if (owner == sl.rank) continue;
+            uint32_t r[16];
+            tmem_ld_16cols(tq + 16 * c, r);
+            tmem_ld_wait();
+            const int slot = (sl.rank - (sl.rank > owner)) * sl.slice + c - owner * sl.slice;
+            const uint32_t to = mapa_shared(ring, sl.step * owner + sl.offset) + static_cast<uint32_t>(slot) * 4 * kUnit;
+            if (mine)
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    st_cluster_v4(to + g * kUnit, r[4 * g], r[4 * g + 1], r[4 * g + 2], r[4 * g + 3]);
+            __syncwarp();
+        }
+    }
+    __syncwarp();
+    cluster_sync();                             // every sum has arrived
+    if (warp_mine) {
+        const float sa = mine ? gsa[row] : 0.0f;
+        const int c0 = sl.rank * sl.slice, end = min(sl.chunks, c0 + sl.slice);
+        for (int c = c0 + half; c < end; c += 2) {
+            uint32_t r[16];
+            tmem_ld_16cols(tq + 16 * c, r);
+            tmem_ld_wait();
+            if (mine) {
+                uint32_t from = ring + static_cast<uint32_t>(c - c0) * 4 * kUnit;
+                for (int i = 1; i < sl.splits; ++i, from += static_cast<uint32_t>(sl.slice) * 4 * kUnit)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const uint4 v = lds128(from + g * kUnit);
+                        r[4 * g] += v.x, r[4 * g + 1] += v.y, r[4 * g + 2] += v.z, r[4 * g + 3] += v.w;
+                    }
+                uint32_t o[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    o[j] = scale_bf16x2(r[2 * j], r[2 * j + 1], sa, s_sw[16 * c + 2 * j], s_sw[16 * c + 2 * j + 1]);
+                const int n0 = n_base + 16 * c;
+                uint16_t* yp = y + static_cast<int64_t>(row) * ldy + n0;
+                if (n0 + 16 <= N) {
+                    *reinterpret_cast<uint4*>(yp) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(yp + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (n0 + j < N) yp[j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
+                }
+            }
+            __syncwarp();
+        }
+    }
+    __syncwarp();
+}
 
 #include "int8_gemm_few.cuh"
 
@@ -56,6 +139,12 @@ constexpr int kEpiWarps = 8;                    // two per TMEM lane quarter
 // TMEM and 128..255 in the odd one's.  Two accumulators of 256 columns each:
 // the epilogue drains one while the MMAs fill the other -- or, with wide tiles
 // of 2 BN columns, both belong to one tile: A is loaded once for the two.
+// With kSplit a cluster of two or four pairs shares a tile's K and each pair owns
+// a slice of its columns, to which the others' sums come through distributed
+// shared memory: for narrow products of long rows, whose k-steps cost the same
+// however narrow the tile is (160 x 5120 x 17408 25 us, 36.8 by whole tiles; 256 x
+// 2048 x 17408 17.9 and 35.5; 384 x 1024 x 28672 23 and 56; but 512 x 5120 x 5120
+// 15.8 whole, 26 shared).
 //   warp 0      TMA producer (both CTAs; bytes counted on the even CTA's barrier)
 //   warp 1      MMA issuer (even CTA), TMEM owner
 //   warps 2..9  epilogue: two warps per TMEM lane quarter take alternate
@@ -93,6 +182,7 @@ struct PairArgs {
     int bn;                                     // columns of an accumulator
     int wide;                                   // 1: a tile fills both accumulators, 2 bn columns
     int stages;
+    int splits;                                 // pairs of a cluster that share a tile's K
     uint64_t timeout_ns;
     int* status;
 };
@@ -104,6 +194,7 @@ __host__ __device__ constexpr int pair_stages(int bn, int wide) {
     return static_cast<int>(kPairRing / pair_stage_bytes(bn, wide)) < kPairMaxStages
                ? static_cast<int>(kPairRing / pair_stage_bytes(bn, wide)) : kPairMaxStages;
 }
+static_assert(kMaxSplits == 8, "BN and its slices are whole chunks of 16 columns for 2 and 4 pairs");
 static_assert(pair_stages(256, 0) >= 6 && pair_stages(256, 1) >= 4, "the widest tiles keep a deep ring");
 static_assert(kPairSmem > 228 * 1024 / 2, "two CTAs could share an SM and its 512 TMEM columns");
 
@@ -118,6 +209,7 @@ __device__ __forceinline__ void pair_tile(int t, const PairArgs& a, int& mt, int
     nt = local / gsize;
 }
 
+template <bool kSplit>
 __global__ void __launch_bounds__(kPairThreads, 1)
 int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                       const __grid_constant__ CUtensorMap tmap_b,
@@ -144,10 +236,16 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();             // 0: issues the pair's MMAs
-    const int pair = blockIdx.x >> 1;
-    const int npairs = gridDim.x >> 1;
+    const uint32_t ctarank = cluster_ctarank();
+    const uint32_t rank = ctarank & 1u;                  // 0: issues the pair's MMAs
+    const uint32_t even = kSplit ? ctarank & ~1u : 0u;   // the pair's even CTA in the cluster
     const int total_tiles = args.m_tiles * args.n_tiles;
+    // this pair's tiles and its k-steps of each: all, or its part of one tile's
+    const int split = static_cast<int>(even >> 1);
+    const int pair = static_cast<int>(blockIdx.x) / (kSplit ? 2 * args.splits : 2);
+    const int npairs = kSplit ? total_tiles : static_cast<int>(gridDim.x >> 1);
+    const int kb0 = kSplit ? split * args.k_steps / args.splits : 0;
+    const int kb1 = kSplit ? (split + 1) * args.k_steps / args.splits : args.k_steps;
     grid_launch_dependents();
 
     if (threadIdx.x == 0) {
@@ -175,8 +273,8 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
     cluster_sync();                                      // barriers of both CTAs initialised
     tc_fence_after();
     const uint32_t tmem_base = *s_tmem_base;
-    const uint32_t full0_leader = mapa_shared(smem_u32(&full[0]), 0);
-    const uint32_t tmem_empty_leader = mapa_shared(smem_u32(tmem_empty), 0);
+    const uint32_t full0_leader = mapa_shared(smem_u32(&full[0]), even);
+    const uint32_t tmem_empty_leader = mapa_shared(smem_u32(tmem_empty), even);
 
     // The two feeding roles run as whole warps with one lane issuing.  A
     // wait that gives up raises `failed`; from then on the role's waits return
@@ -190,8 +288,8 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
         // L2 (a hint: nothing of it is read before the wait).
         const bool once = args.m_tiles == 1;
         if (leader && once) {
-            const int ahead = min(STAGES, args.k_steps);
-            for (int kb = 0; kb < ahead; ++kb)
+            const int ahead = min(kb0 + STAGES, kb1);
+            for (int kb = kb0; kb < ahead; ++kb)
                 for (int h = 0; h <= wide; ++h)
                     tma_prefetch_2d(&tmap_b, kb * kStepBytes,
                                     pair * TN + h * BN + static_cast<int>(rank) * (BN / 2));
@@ -208,7 +306,7 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             pair_tile(t, args, mt, nt);
             const int ya = mt * 256 + static_cast<int>(rank) * kRows;
             const int yb = nt * TN + static_cast<int>(rank) * (BN / 2);
-            for (int kb = 0; kb < args.k_steps; ++kb) {
+            for (int kb = kb0; kb < kb1; ++kb) {
                 if (!ready) failed |= !mbar_spin(empty0 + 8 * stage, phase ^ 1u, failed ? 1 : kSpinTries);
                 const int next = stage + 1 == STAGES ? 0 : stage + 1;
                 const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
@@ -261,7 +359,7 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 if (wide) failed |= !mbar_spin(acc_empty0 + 8, acc_phase ^ 1u, failed ? 1 : kSpinTries);
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * 256;
-                for (int kb = 0; kb < args.k_steps; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!ready) failed |= !mbar_spin(full0 + 8 * stage, phase, failed ? 1 : kSpinTries);
                     tc_fence_after();
                     const int next = stage + 1 == STAGES ? 0 : stage + 1;
@@ -276,19 +374,19 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                         for (int j = 0; j < kStepBytes / 32; ++j)
                             if (j < nmma)
                                 tc_mma_i8_pair(d_tmem, da + 2 * j, db + 2 * j, idesc,
-                                               static_cast<uint32_t>(kb | j));
+                                               static_cast<uint32_t>((kb - kb0) | j));
                         if (wide) {
                             const uint64_t db1 = db + (HALF_B >> 4);
 #pragma unroll
                             for (int j = 0; j < kStepBytes / 32; ++j)
                                 if (j < nmma)
                                     tc_mma_i8_pair(tmem_base + 256, da + 2 * j, db1 + 2 * j, idesc,
-                                                   static_cast<uint32_t>(kb | j));
+                                                   static_cast<uint32_t>((kb - kb0) | j));
                         }
-                        tc_commit_pair(&empty[stage], 0x3);
-                        if (kb == last_kb) {
-                            tc_commit_pair(&tmem_full[acc], 0x3);
-                            if (wide) tc_commit_pair(&tmem_full[1], 0x3);
+                        tc_commit_pair(&empty[stage], 0x3 << even);
+                        if (kb == kb1 - 1) {
+                            tc_commit_pair(&tmem_full[acc], 0x3 << even);
+                            if (wide) tc_commit_pair(&tmem_full[1], 0x3 << even);
                         }
                     }
                     __syncwarp();
@@ -309,12 +407,21 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             }
             __syncwarp();
             if (elect_one()) {
-                tc_commit_pair(drain, 0x1);
+                tc_commit_pair(drain, 0x1 << even);
                 int local_abort = 0;
                 mbar_wait_bounded(drain, 0, args.timeout_ns, &local_abort, args.status);
             }
             __syncwarp();
         }
+    } else if constexpr (kSplit) {
+        // ---------------- epilogue (warps 2..9): this pair's sums are complete ----------------
+        const int tid = threadIdx.x - 64;
+        int mt, nt;
+        pair_tile(pair, args, mt, nt);
+        grid_dependency_wait();
+        reinterpret_cast<float*>(epi)[tid] = tid < BN && nt * BN + tid < args.N ? args.sw[nt * BN + tid] : 0.0f;
+        mbar_wait_warp(&tmem_full[0], 0, args.timeout_ns, s_abort, args.status);
+        __syncwarp();
     } else {
         // ---------------- epilogue (warps 2..9, both CTAs) ----------------
         grid_dependency_wait();
@@ -403,6 +510,16 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
         // every store of this warp has completed before the CTA exits
         if (lane == 0) bulk_wait_all();
         __syncwarp();
+    }
+
+    if constexpr (kSplit) {
+        int mt, nt;
+        pair_tile(pair, args, mt, nt);
+        const int m = (warp & 3) * 32 + lane;
+        const Slices sl = {args.splits, split, 2, static_cast<int>(rank), BN / 16 / args.splits,
+                           min(BN, args.N - nt * BN + 15) / 16};
+        exchange_and_store(sl, tmem_base, smem_u32(smem), reinterpret_cast<const float*>(epi), args.sa, args.y,
+                           args.ldy, m, mt * 256 + static_cast<int>(rank) * kRows + m, args.M, 32, nt * BN, args.N);
     }
 
     tc_fence_before();
@@ -548,9 +665,10 @@ nvfp4_status launch_few(const Operands& o, const DeviceInfo& info, int* status, 
     // (48 bytes a cycle); memory as a whole delivers some 3400 bytes of weights
     // a cycle.  The slower of the two decides; a quarter of the SMs' share is
     // added, so that among widths that memory bounds the least loaded SMs win.
-    // Sharing K among the CTAs of a cluster costs 3500 and the exchange of the
-    // sums, 10 bytes a cycle.  Measured for 90 shapes of up to 128 tokens, the
-    // choice takes 1 % longer than the best of all widths and splits on average.
+    // Sharing K among the CTAs of a cluster costs 3000 and 200 for each of them,
+    // and the exchange of the sums, 10 bytes a cycle.  Measured for 90 shapes of
+    // up to 128 tokens, the choice takes 1 % longer than the best of all widths
+    // and splits on average, 17 % at the worst (of 3.6 us).
     int u = 0;
     int64_t best = 0;
     const int64_t memory = o.N * static_cast<int64_t>(kStepBytes) / 3400;
@@ -567,7 +685,7 @@ nvfp4_status launch_few(const Operands& o, const DeviceInfo& info, int* status, 
                                           (f.nt + bn) * kStepBytes / 48);
             const int64_t sm = (tiles + fit - 1) / fit * step / splits;
             const int64_t cost = f.k_steps * (std::max(sm, memory) + sm / 4) +
-                                 (splits > 1 ? 3500 + f.nt * bn * 4 * (splits - 1) / splits / 10 : 0);
+                                 (splits > 1 ? 3000 + 200 * splits + f.nt * bn * 4 * (splits - 1) / splits / 10 : 0);
             if (best == 0 || cost < best) best = cost, f.bn = bn, f.stages = bs, f.splits = splits, u = bu;
         }
     }
@@ -585,13 +703,26 @@ nvfp4_status launch_few(const Operands& o, const DeviceInfo& info, int* status, 
 }
 
 nvfp4_status launch_pair(const Operands& o, const DeviceInfo& info, int* status, cudaStream_t stream) {
-    auto kern = int8_gemm_pair_kernel;
+    using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, PairArgs);
+    static const Kernel kernels[2] = {int8_gemm_pair_kernel<false>, int8_gemm_pair_kernel<true>};
     static PerDeviceOnce once;
+    static int resident[kMaxDevices][kMaxSplits / 2 + 1];  // clusters of 2 and 4 pairs that fit the device
     int dev = 0;
     nvfp4_status st = current_device(&dev);
     if (st != NVFP4_OK) return st;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
     st = once.run(dev, [&] {
-        return cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem));
+        for (const Kernel k : kernels)
+            if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem) != cudaSuccess)
+                return NVFP4_ERR_CUDA;
+        for (int s = 2; s <= kMaxSplits / 2; s *= 2) {
+            launch_config(&cfg, attr, 2 * s, kPairThreads, kPairSmem, nullptr);
+            cfg.gridDim = dim3(static_cast<unsigned>(info.sms / (2 * s) * (2 * s)), 1, 1);
+            if (cudaOccupancyMaxActiveClusters(&resident[dev][s], kernels[1], &cfg) != cudaSuccess)
+                return NVFP4_ERR_CUDA;
+        }
+        return NVFP4_OK;
     });
     if (st != NVFP4_OK) return st;
     PairArgs p = {};
@@ -601,42 +732,50 @@ nvfp4_status launch_pair(const Operands& o, const DeviceInfo& info, int* status,
     p.timeout_ns = kTimeoutNs;
     p.status = status;
     const int max_pairs = info.sms / 2;
-    // Tile width, by cycles of shared memory, which the copies' writes and the
-    // MMAs' reads share at 128 bytes a cycle: a k-step of BN columns writes 128 +
-    // BN / 2 rows of 128 bytes and reads 128 + BN; a wide one, of 2 BN columns,
-    // writes 128 + BN rows and reads twice 128 + BN, which is less than two
-    // narrow ones, but no MMAs overlap its epilogue (some 16 BN cycles an
-    // accumulator; of narrow tiles the last one's counts).  Take the width whose
-    // rounds of tiles cost least, the widest among equals.  (Measured for 1000 x
-    // 5120 x 17408, cycles a k-step: 393, 483, 519, 532 and 583 for BN = 128 to
-    // 256, against 448 to 640 by this rule; the product takes 61 us in wide tiles
-    // of 320 columns, one round, and 70 in narrow ones of 160, two rounds.)
+    // Tile width and the split of K, by cycles of shared memory, which the
+    // copies' writes and the MMAs' reads share at 128 bytes a cycle: a k-step of BN
+    // columns writes 128 + BN / 2 rows of 128 bytes and reads 128 + BN (450 cycles
+    // at the least); a wide one, of 2 BN columns, writes 128 + BN rows and reads
+    // twice 128 + BN, which is less than two narrow ones, but no MMAs overlap its
+    // epilogue (28 BN cycles; of narrow tiles the last one's 16 BN count).  A round of tiles costs 1500 besides; sharing K among pairs 2000
+    // and the exchange of the sums, 10 bytes a cycle.  Take what costs least, the
+    // widest among equals.  (Measured for 1000 x 5120 x 17408, cycles a k-step:
+    // 393, 483, 519, 532 and 583 for BN = 128 to 256; the product takes 61 us in
+    // wide tiles of 320 columns, one round, and 70 in narrow ones of 160, two
+    // rounds.  Over 130 shapes of 129 to 2500 tokens the choice takes 1 % longer than
+    // the best on average, 10 % at the worst.)
     int64_t best = 0;
-    for (int wide = 1; wide >= 0; --wide)
-        for (int bn = kPairMaxBN; bn >= (wide ? 160 : 64); bn -= 32) {
-            const int64_t tiles = static_cast<int64_t>(p.m_tiles) * ((o.N + (bn << wide) - 1) / (bn << wide));
-            const int64_t rounds = (tiles + max_pairs - 1) / max_pairs;
-            const int64_t cost = wide ? rounds * (p.k_steps * int64_t(384 + 3 * bn) + 32 * bn)
-                                      : rounds * p.k_steps * (256 + 3 * bn / 2) + 16 * bn;
-            if (best == 0 || cost < best) best = cost, p.bn = bn, p.wide = wide;
-        }
+    for (int splits = 1; splits <= kMaxSplits / 2; splits *= 2) {
+        const int fit = splits == 1 ? max_pairs : resident[dev][splits];
+        if (fit <= 0 || p.k_steps < splits) continue;
+        for (int wide = splits == 1; wide >= 0; --wide)
+            for (int bn = kPairMaxBN; bn >= (wide ? 160 : 64); bn -= splits < 4 ? 32 : 64) {
+                const int64_t tiles = static_cast<int64_t>(p.m_tiles) * ((o.N + (bn << wide) - 1) / (bn << wide));
+                const int64_t rounds = (tiles + fit - 1) / fit;
+                const int64_t step = wide ? 384 + 3 * bn : std::max(256 + 3 * bn / 2, 450);
+                int64_t cost = rounds * (p.k_steps * step / splits + 1500);
+                if (splits > 1)
+                    cost += rounds * (2000 + kRows * bn * 4 * (splits - 1) / splits / 10);
+                else
+                    cost += wide ? rounds * 28 * bn : 16 * bn;
+                if (best == 0 || cost < best) best = cost, p.bn = bn, p.wide = wide, p.splits = splits;
+            }
+    }
     p.n_tiles = (o.N + (p.bn << p.wide) - 1) / (p.bn << p.wide);
     p.stages = pair_stages(p.bn, p.wide);
     // Raster: when A fits comfortably in L2, sweep every M tile for each N tile
     // (the weight then streams from HBM once); otherwise bands of 16 M tiles.
     p.group_m = static_cast<int64_t>(o.M) * o.K <= (int64_t(48) << 20) ? 1 << 30 : 16;
     const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
-    const int pairs = static_cast<int>(std::min<int64_t>(tiles, max_pairs));
+    const int pairs = static_cast<int>(p.splits > 1 ? tiles * p.splits : std::min<int64_t>(tiles, max_pairs));
     CUtensorMap ta, tb, ty;
     if (!make_codes_map(&ta, o.a, o.M, o.K, kRows) || !make_codes_map(&tb, o.w, o.N, o.K, p.bn / 2) ||
         !make_map(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, o.y, o.M, o.N, o.ldy * 2, 32, 32,
                   CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE))
         return NVFP4_ERR_CUDA;
-    cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr[2];
-    launch_config(&cfg, attr, 2, kPairThreads, kPairSmem, stream);
+    launch_config(&cfg, attr, 2 * p.splits, kPairThreads, kPairSmem, stream);
     cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
-    if (cudaLaunchKernelEx(&cfg, kern, ta, tb, ty, p) != cudaSuccess) return NVFP4_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kernels[p.splits > 1], ta, tb, ty, p) != cudaSuccess) return NVFP4_ERR_CUDA;
     return cuda_status(cudaGetLastError());
 }
 

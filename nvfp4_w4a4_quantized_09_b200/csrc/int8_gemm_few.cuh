@@ -4,10 +4,10 @@
 // Tiles of all the tokens x BN channels, in one of three ways:
 //   * The tokens are the MMA's rows (64 of them up to 64 tokens, then 128) and
 //     the channels its N = BN, a multiple of 16 up to 256.  BN is free, so the
-//     launcher picks it to fill whole rounds of the SMs.  Only the tokens' own rows are loaded (NT = M rounded up to
-//     8); the MMA reads all its rows from the tile's start, those beyond NT are
-//     whatever shared memory holds there, and the accumulator lanes they fill
-//     are never read.
+//     launcher picks it to fill whole rounds of the SMs.  Only the tokens' own
+//     rows are loaded (NT = M rounded up to 8); the MMA reads all its rows from
+//     the tile's start, those beyond NT are whatever shared memory holds there,
+//     and the accumulator lanes they fill are never read.
 //   * kSwap, for M <= 32 and 224 channels an SM or more: the channels are the
 //     MMA's 64 or 128 rows and the tokens its N = 16 or 32.  The same weight
 //     bytes then take a quarter to a half of the multiplications, and with them
@@ -25,11 +25,12 @@
 //     100 x 5120 x 17408 19.7 us, 27.0 by whole tiles; 128 x 2048 x 17408 12.0
 //     and 24.8; 16 x 2048 x 17408 9.5 and 13.3; 1 x 256 x 17408 6.9 and 12.3;
 //     but 64 x 5120 x 5120 8.4 and 8.0, which stays whole.
-// Common to both:
+// Common to all:
 //   * A pipeline stage holds U = 1, 2, 4 or 8 steps of 128 values of K, the
 //     most that 58 KB take: each stage costs the MMA warp a handshake during
 //     which the tensor pipe idles, and each operand one copy.
-//   * Persistent: the ring runs across tiles, two accumulators of 256 columns.
+//   * Persistent (but for kSplit, one tile a cluster): the ring runs across
+//     tiles, two accumulators of 256 columns.
 //   * Launched as a programmatic dependent: every role that touches global
 //     memory first waits for the previous grid (griddepcontrol.wait); the
 //     first ring of weights is prefetched into L2 before that (5 to 7 % of a
@@ -49,7 +50,6 @@ constexpr int kFewMaxTokens = 128;
 constexpr int kSwapTokens = 32;                      // at most: channels as the MMA's rows
 constexpr int kFewMaxStages = 16;
 constexpr int kFewMaxBN = 256;
-constexpr int kMaxSplits = 8;                        // CTAs of a cluster that share a tile's K
 constexpr uint32_t kFewSmem = 227 * 1024;            // whole: one CTA per SM
 constexpr uint32_t kFewBars = (2 * kFewMaxStages + 5) * 8;
 constexpr uint32_t kFewScales = 2 * kFewMaxBN * 4;    // channel scales, one set per accumulator
@@ -408,76 +408,10 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
     }
 
     if constexpr (kSplit) {
-        // The CTAs of the cluster own a slice of the tile's columns each.  Every
-        // CTA stores its sums of the other slices into their owners' shared
-        // memory, where the ring has served; the owner adds them to its own.
-        // Integers: the order is free.  Lanes are tokens, 16 bytes of a token
-        // apart by 16 bytes: a warp's store is 512 consecutive bytes.
-        cluster_sync();                                  // every ring has been read
-        tc_fence_after();
-        const int q = warp & 3, half = (warp - 2) >> 2;
-        const int per_q = args.nt <= 64 ? 16 : 32;
-        const int m = q * per_q + lane;
-        const bool warp_mine = warp >= 2 && q * per_q < args.M;
-        const bool mine = warp_mine && lane < per_q && m < args.M;
-        const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-        const int slice = BN / 16 / args.splits;         // chunks of 16 columns
-        const int chunks = min(BN, args.N - first * BN + 15) / 16;
-        const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(m) * 16;
-        constexpr uint32_t kUnit = kRows * 16;           // 4 columns of all tokens
-        if (warp_mine) {
-            for (int c = half; c < chunks; c += 2) {
-                const int owner = c / slice;
-                if (owner == rank) continue;
-                uint32_t r[16];
-                tmem_ld_16cols(tq + 16 * c, r);
-                tmem_ld_wait();
-                const int slot = (rank - (rank > owner)) * slice + c - owner * slice;
-                const uint32_t to = mapa_shared(ring, owner) + static_cast<uint32_t>(slot) * 4 * kUnit;
-                if (mine)
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        st_cluster_v4(to + g * kUnit, r[4 * g], r[4 * g + 1], r[4 * g + 2], r[4 * g + 3]);
-                __syncwarp();
-            }
-        }
-        __syncwarp();
-        cluster_sync();                                  // every sum has arrived
-        if (warp_mine) {
-            const float sa = mine ? args.sa[m] : 0.0f;
-            const int end = min(chunks, (rank + 1) * slice);
-            for (int c = rank * slice + half; c < end; c += 2) {
-                uint32_t r[16];
-                tmem_ld_16cols(tq + 16 * c, r);
-                tmem_ld_wait();
-                if (mine) {
-                    uint32_t from = ring + static_cast<uint32_t>(c - rank * slice) * 4 * kUnit;
-                    for (int i = 1; i < args.splits; ++i, from += static_cast<uint32_t>(slice) * 4 * kUnit)
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const uint4 v = lds128(from + g * kUnit);
-                            r[4 * g] += v.x, r[4 * g + 1] += v.y, r[4 * g + 2] += v.z, r[4 * g + 3] += v.w;
-                        }
-                    uint32_t o[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        o[j] = scale_bf16x2(r[2 * j], r[2 * j + 1], sa, s_scales[16 * c + 2 * j],
-                                            s_scales[16 * c + 2 * j + 1]);
-                    const int n0 = first * BN + 16 * c;
-                    uint16_t* yp = args.y + static_cast<int64_t>(m) * args.ldy + n0;
-                    if (n0 + 16 <= args.N) {
-                        *reinterpret_cast<uint4*>(yp) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4*>(yp + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (n0 + j < args.N) yp[j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
-                    }
-                }
-                __syncwarp();
-            }
-        }
-        __syncwarp();
+        const int m = (warp & 3) * (args.nt <= 64 ? 16 : 32) + lane;
+        const Slices sl = {args.splits, rank, 1, 0, BN / 16 / args.splits, min(BN, args.N - first * BN + 15) / 16};
+        exchange_and_store(sl, tmem_base, smem_u32(smem), s_scales, args.sa, args.y, args.ldy, m, m, args.M,
+                           args.nt <= 64 ? 16 : 32, first * BN, args.N);
     }
 
     tc_fence_before();

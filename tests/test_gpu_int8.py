@@ -332,7 +332,11 @@ def test_gemm_configurations(M, N, K):
     (1, 256, 17408), (3, 169, 27056), (7, 300, 8192), (16, 80, 131056), (20, 6819, 10864), (33, 1024, 28672),
     (34, 1, 10128), (55, 579, 13600), (64, 2051, 8208), (64, 5120, 17408), (65, 80, 22080), (65, 1000, 5136),
     (97, 6738, 19776), (100, 5120, 17408), (104, 4867, 25488), (114, 1111, 2544), (121, 517, 17424),
-    (128, 2048, 17408), (128, 8, 131056), (128, 8192, 17408)])
+    (128, 2048, 17408), (128, 8, 131056), (128, 8192, 17408),
+    # ... and among CTA pairs, two and four of them, of one M tile and several
+    (129, 256, 17408), (160, 2048, 17408), (200, 5120, 17408), (256, 1024, 28672), (256, 2051, 8208),
+    (257, 80, 22080), (300, 517, 17424), (384, 5120, 17408), (500, 1000, 5136), (511, 1, 131056),
+    (512, 5120, 5120), (700, 300, 27056), (1000, 256, 17408)])
 def test_gemm_shares_long_rows_among_ctas(M, N, K):
     a, w = gemm_inputs(M, N, K, seed=M + K)
     y = torch.full((M, (N + 23) // 8 * 8), 7.0, dtype=BF, device=DEV)
