@@ -746,6 +746,7 @@ PROFILE_CASES = {
     "harmonize_gdn": "harmonisation of the fused GDN weight's scales [24704,5120], in place",
     "int8_gemm_gateup": "int8 GEMM, A [8192,5120] x W [34816,5120]",
     "int8_gemm_decode": "int8 GEMM, A [8,5120] x W [34816,5120]",
+    "int8_gemm_down": "int8 GEMM, A [100,17408] x W [5120,17408] (K shared by clusters of CTAs)",
     "int8_norm": "residual addition, RMS norm and int8 codes of [32768,5120]",
     "int8_quantize": "int8 codes of the MLP intermediate [8192,17408]",
 }
@@ -800,11 +801,12 @@ def run_profile_case(case: str, launches: int) -> None:
         torch.cuda.synchronize()
         for _ in range(launches):
             nv.harmonize(fw)
-    elif case in ("int8_gemm_gateup", "int8_gemm_decode"):
-        M = 8192 if case == "int8_gemm_gateup" else 8
-        a = nv.int8_quantize_tensor(synth.student_t_activations(M, K_HID, seed=1, device=dev))
-        w = nv.int8_quantize_tensor(synth.gaussian_weights(34816, K_HID, 0.015, seed=20, device=dev))
-        y = torch.empty(M, 34816, dtype=torch.bfloat16, device=dev)
+    elif case in ("int8_gemm_gateup", "int8_gemm_decode", "int8_gemm_down"):
+        M, N, K = {"int8_gemm_gateup": (8192, 34816, K_HID), "int8_gemm_decode": (8, 34816, K_HID),
+                   "int8_gemm_down": (100, 5120, 17408)}[case]
+        a = nv.int8_quantize_tensor(synth.student_t_activations(M, K, seed=1, device=dev))
+        w = nv.int8_quantize_tensor(synth.gaussian_weights(N, K, 0.015, seed=20, device=dev))
+        y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
         torch.cuda.synchronize()
         for _ in range(launches):
             nv.int8_gemm(a, w, y)

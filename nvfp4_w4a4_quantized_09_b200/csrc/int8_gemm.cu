@@ -47,14 +47,24 @@ constexpr int kEpiWarps = 8;                    // two per TMEM lane quarter
 constexpr int kMaxSplits = 8;                   // CTAs of a cluster that share a tile's K
 
 // A tile whose K the CTAs of a cluster share: `splits` of them (in the pair
-// kernel pairs of them) hold sums of 128 rows x 16 * slice * splits columns in
-// TMEM, and number r owns the r-th slice.
+// kernel pairs of them) hold sums of 128 rows x BN columns in TMEM, and number r
+// owns the r-th slice (the last ones may be shorter, or empty).
 struct Slices {
     int splits, rank;
     int step, offset;                           // owner r is CTA step * r + offset of the cluster
     int slice;                                  // chunks of 16 columns each owns
     int chunks;                                 // of the tile inside the matrix
 };
+__host__ __device__ constexpr int slice_chunks(int bn, int splits) { return (bn / 16 + splits - 1) / splits; }
+// What an owner's shared memory takes in: 8 KB a chunk from each of the others.
+constexpr uint32_t kMaxExchange = 7 * 2 * 8192;
+constexpr bool exchanges_fit() {
+    for (int splits = 2; splits <= kMaxSplits; splits *= 2)
+        for (int bn = 16; bn <= 256; bn += 16)
+            if (static_cast<uint32_t>(splits - 1) * slice_chunks(bn, splits) * 8192 > kMaxExchange) return false;
+    return true;
+}
+static_assert(exchanges_fit(), "the sums of a tile do not fit where its ring was");
 
 // By all threads of every CTA of the cluster, once its sums are complete.  Every
 // CTA stores its sums of the other slices into their owners' shared memory,
@@ -143,7 +153,7 @@ __device__ __forceinline__ void exchange_and_store(const Slices& sl, uint32_t tm
 // a slice of its columns, to which the others' sums come through distributed
 // shared memory: for narrow products of long rows, whose k-steps cost the same
 // however narrow the tile is (160 x 5120 x 17408 25 us, 36.8 by whole tiles; 256 x
-// 2048 x 17408 17.9 and 35.5; 384 x 1024 x 28672 23 and 56; but 512 x 5120 x 5120
+// 2048 x 17408 16.8 and 35.4; 384 x 1024 x 28672 23 and 56; but 512 x 5120 x 5120
 // 15.8 whole, 26 shared).
 //   warp 0      TMA producer (both CTAs; bytes counted on the even CTA's barrier)
 //   warp 1      MMA issuer (even CTA), TMEM owner
@@ -194,7 +204,7 @@ __host__ __device__ constexpr int pair_stages(int bn, int wide) {
     return static_cast<int>(kPairRing / pair_stage_bytes(bn, wide)) < kPairMaxStages
                ? static_cast<int>(kPairRing / pair_stage_bytes(bn, wide)) : kPairMaxStages;
 }
-static_assert(kMaxSplits == 8, "BN and its slices are whole chunks of 16 columns for 2 and 4 pairs");
+static_assert(kPairRing >= kMaxExchange, "the ring takes in the other pairs' sums");
 static_assert(pair_stages(256, 0) >= 6 && pair_stages(256, 1) >= 4, "the widest tiles keep a deep ring");
 static_assert(kPairSmem > 228 * 1024 / 2, "two CTAs could share an SM and its 512 TMEM columns");
 
@@ -516,7 +526,7 @@ int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
         int mt, nt;
         pair_tile(pair, args, mt, nt);
         const int m = (warp & 3) * 32 + lane;
-        const Slices sl = {args.splits, split, 2, static_cast<int>(rank), BN / 16 / args.splits,
+        const Slices sl = {args.splits, split, 2, static_cast<int>(rank), slice_chunks(BN, args.splits),
                            min(BN, args.N - nt * BN + 15) / 16};
         exchange_and_store(sl, tmem_base, smem_u32(smem), reinterpret_cast<const float*>(epi), args.sa, args.y,
                            args.ldy, m, mt * 256 + static_cast<int>(rank) * kRows + m, args.M, 32, nt * BN, args.N);
@@ -674,9 +684,9 @@ nvfp4_status launch_few(const Operands& o, const DeviceInfo& info, int* status, 
     const int64_t memory = o.N * static_cast<int64_t>(kStepBytes) / 3400;
     const int max_splits = swap ? 1 : kMaxSplits;
     for (int splits = 1; splits <= max_splits; splits *= 2) {
-        const int unit = swap ? 64 : 16 * splits, fit = splits == 1 ? info.sms : resident[dev][splits];
+        const int unit = swap ? 64 : 16, fit = splits == 1 ? info.sms : resident[dev][splits];
         if (fit <= 0) continue;
-        for (int bn = unit; bn <= (swap ? 128 : kFewMaxBN); bn += unit) {
+        for (int bn = swap ? 64 : 16 * splits; bn <= (swap ? 128 : kFewMaxBN); bn += unit) {
             const int64_t tiles = (o.N + bn - 1) / bn;
             int bu = 0, bs = 0;
             few_config(f.nt, bn, &bu, &bs);
@@ -749,7 +759,7 @@ nvfp4_status launch_pair(const Operands& o, const DeviceInfo& info, int* status,
         const int fit = splits == 1 ? max_pairs : resident[dev][splits];
         if (fit <= 0 || p.k_steps < splits) continue;
         for (int wide = splits == 1; wide >= 0; --wide)
-            for (int bn = kPairMaxBN; bn >= (wide ? 160 : 64); bn -= splits < 4 ? 32 : 64) {
+            for (int bn = kPairMaxBN; bn >= (wide ? 160 : 64); bn -= 32) {
                 const int64_t tiles = static_cast<int64_t>(p.m_tiles) * ((o.N + (bn << wide) - 1) / (bn << wide));
                 const int64_t rounds = (tiles + fit - 1) / fit;
                 const int64_t step = wide ? 384 + 3 * bn : std::max(256 + 3 * bn / 2, 450);
