@@ -24,12 +24,13 @@
 // 2 + 1 written), 3 without and for the plain quantizer.  On a B200 (copies run
 // at 6.55 TB/s), CUDA-graph replay over rotating inputs:
 //   norm  32768 x 5120 182 us = 6.4 TB/s, 8192 x 5120 47.7 us = 6.2,
-//         16384 x 8192 148 us = 6.4, 8192 x 17408 193 us = 5.2 (one CTA of 96
-//         registers per SM), 4096 x 32768 204 us = 4.6 (staged in shared
-//         memory; 240 with a second pass over the row);
-//         without a residual 8192 x 5120 26 us = 4.8 (by then the instructions)
+//         16384 x 8192 148 us = 6.4, 8192 x 17408 160-164 us = 6.1-6.3, 4096 x
+//         32768 190 us = 4.9 (staged in shared memory; 240 with a second pass
+//         over the row), 1000 x 131072 262 us = 3.5 (two passes);
+//         without a residual 8192 x 5120 26 us = 4.8 (by then the instructions:
+//         fewer registers and more CTAs are slower), 4096 x 32768 81 us = 5.0
 //   plain 8191 x 17408 67.6 us = 6.3, 8192 x 5120 21.6 us = 5.8, 4096 x 32768
-//         62 us = 6.5
+//         62 us = 6.5, 3000 x 49152 81 us = 5.5 (staged)
 //   one row of 5120 2.2 us, eight of 17408 2.1 us
 // What brought it there: one pass with the next row's loads in flight during
 // the reduction (norm 8192 x 5120: 70.6 us in two passes); the plain row held
@@ -85,6 +86,13 @@ __device__ __forceinline__ uint4 ld_row16(const uint16_t* p) {
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
+    return v;
+}
+
+// Eight weights, again for every row: volatile, or the compiler would keep them.
+__device__ __forceinline__ uint4 ld_weight(const uint16_t* p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
 
@@ -188,10 +196,15 @@ __device__ __forceinline__ bool finish_row(const RowArgs& a, int64_t row, float 
 // Rows that fit a CTA's registers: V vectors of 8 per thread, the vectors of a
 // thread blockDim.x apart.  Each CTA walks rows, and the next row's loads leave
 // before the current row's reduction.  Between that and the encoding the norm
-// holds t (with its weights in registers); without a norm the row is held as
-// loaded.  What counts is bytes in flight: thread counts and register limits
-// are set so that two CTAs or more share an SM where that is possible.
-constexpr int row_max_threads(bool norm, int v) { return v == 2 ? (norm ? 1024 : 768) : 640; }
+// holds t (and with V = 2 its weights, which longer rows read from L1 again);
+// without a norm the row is held as loaded.  What counts is bytes in flight and
+// warps: thread counts and register limits are set so that two CTAs or more
+// share an SM where that is possible, or one has up to 32 warps (norm with a
+// residual, 8192 x 17408: 191 us with V = 4 and the weights held, in 17 warps;
+// 164 with V = 3 in 23.  Reading the weights again with V = 2: 8192 x 5120 without a
+// residual 34 us against 26.  A row shared by a cluster of CTAs: a cluster
+// barrier a row, 301 us for 8192 x 17408).
+constexpr int row_max_threads(bool norm, int v) { return norm ? 1024 : v == 2 ? 768 : 640; }
 constexpr int row_min_ctas(bool norm, int v) { return norm || v == 8 ? 1 : 2; }
 
 template <bool kNorm, bool kRes, int V>
@@ -202,12 +215,13 @@ __global__ void __launch_bounds__(row_max_threads(kNorm, V), row_min_ctas(kNorm,
     const int vecs = a.cols / 8;
     const int warps = blockDim.x >> 5;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    uint4 w[V], xv[V], rv[V];
+    constexpr bool kHeld = V == 2;                  // the weights stay in registers
+    uint4 w[kHeld ? V : 1], xv[V], rv[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int v = threadIdx.x + j * blockDim.x;
         const bool in = v < vecs;
-        w[j] = kNorm && in ? *reinterpret_cast<const uint4*>(a.weight + 8 * v) : zero;
+        if (kHeld) w[j] = kNorm && in ? *reinterpret_cast<const uint4*>(a.weight + 8 * v) : zero;
         xv[j] = in ? ld_row16(a.x + blockIdx.x * a.ldx + 8 * v) : zero;
         rv[j] = kRes && in ? ld_row16(a.residual + blockIdx.x * a.ldr + 8 * v) : zero;
     }
@@ -222,9 +236,12 @@ __global__ void __launch_bounds__(row_max_threads(kNorm, V), row_min_ctas(kNorm,
             if constexpr (kNorm) {
                 float r[8];
                 sum_r<kRes>(xv[j], rv[j], r);
-                weigh<kNorm>(w[j], a.weight_offset, r, t[j]);
-                tally<kNorm>(r, t[j], sum, top);
                 const int v = threadIdx.x + j * blockDim.x;
+                if constexpr (kHeld)
+                    weigh<kNorm>(w[j], a.weight_offset, r, t[j]);
+                else
+                    weigh<kNorm>(v < vecs ? ld_weight(a.weight + 8 * v) : zero, a.weight_offset, r, t[j]);
+                tally<kNorm>(r, t[j], sum, top);
                 if (kRes && v < vecs && a.residual_out)
                     *reinterpret_cast<uint4*>(a.residual_out + row * a.ldo + 8 * v) = pack8(r);
             } else {
@@ -267,20 +284,23 @@ __global__ void __launch_bounds__(row_max_threads(kNorm, V), row_min_ctas(kNorm,
 
 // Longer rows: t waits in shared memory (as x itself, in 16 bits, without a
 // norm) between the reduction and the encoding.  Each thread reads back what it
-// wrote; several CTAs per SM keep loads in flight.
-constexpr int kLongThreads = 512;
+// wrote.  Two CTAs of 512 threads share an SM where their rows fit, else one has
+// 1024 (norm 4096 x 32768: 188 us, 214 with 512; plain 3000 x 49152: 81 us with two
+// CTAs, 103 with one).  Beyond shared memory the row is read twice.
+constexpr int kLongThreads = 1024;              // half of them where two CTAs share an SM
+constexpr int kHalfSmem = 112 * 1024;
 constexpr int kLongBatch = 4;
 constexpr int kLongSmem = 200 * 1024;
 
 template <bool kNorm, bool kRes, bool kStaged>
-__global__ void __launch_bounds__(kLongThreads, 2) row_int8_long_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(kLongThreads, 1) row_int8_long_kernel(const RowArgs a) {
     __shared__ uint2 s_red[2][32];
     extern __shared__ uint4 s_row[];
     // rows of any length: the next grid is let in early only where this one is
     // short beside the bounded waits of the kernels that may follow
     if (kStaged) grid_launch_dependents();
     grid_dependency_wait();
-    const int vecs = a.cols / 8;
+    const int vecs = a.cols / 8, threads = blockDim.x;
     const uint4 zero = make_uint4(0, 0, 0, 0);
     int buf = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, buf ^= 1) {
@@ -289,19 +309,19 @@ __global__ void __launch_bounds__(kLongThreads, 2) row_int8_long_kernel(const Ro
         uint16_t* out = kRes && a.residual_out ? a.residual_out + row * a.ldo : nullptr;
         float sum = 0.0f;
         uint32_t top = 0;
-        for (int v0 = threadIdx.x; v0 < vecs; v0 += kLongThreads * kLongBatch) {
+        for (int v0 = threadIdx.x; v0 < vecs; v0 += threads * kLongBatch) {
             uint4 xv[kLongBatch], rv[kLongBatch];
 #pragma unroll
             for (int j = 0; j < kLongBatch; ++j) {
-                const int64_t at = 8 * static_cast<int64_t>(v0 + j * kLongThreads);
-                if (v0 + j * kLongThreads < vecs) {
+                const int64_t at = 8 * static_cast<int64_t>(v0 + j * threads);
+                if (v0 + j * threads < vecs) {
                     xv[j] = ld_row16(x + at);
                     rv[j] = kRes ? ld_row16(res + at) : zero;
                 }
             }
 #pragma unroll
             for (int j = 0; j < kLongBatch; ++j) {
-                const int v = v0 + j * kLongThreads;
+                const int v = v0 + j * threads;
                 const int64_t at = 8 * static_cast<int64_t>(v);
                 if (v >= vecs) break;
                 if constexpr (kNorm) {
@@ -324,10 +344,10 @@ __global__ void __launch_bounds__(kLongThreads, 2) row_int8_long_kernel(const Ro
             }
         }
         if constexpr (!kNorm) top = top_bits(top);
-        reduce_row<kNorm>(sum, top, s_red[buf], kLongThreads / 32);
+        reduce_row<kNorm>(sum, top, s_red[buf], threads / 32);
         float mult;
         const bool ok = finish_row<kNorm>(a, row, sum, top, &mult);
-        for (int v = threadIdx.x; v < vecs; v += kLongThreads) {
+        for (int v = threadIdx.x; v < vecs; v += threads) {
             const int64_t at = 8 * static_cast<int64_t>(v);
             float t[8];
             if constexpr (kStaged && kNorm) {
@@ -409,7 +429,10 @@ nvfp4_status launch_rows(const RowArgs& a, void* stream) {
     if (st != NVFP4_OK) return st;
     // the fewest vectors per thread whose threads fit a CTA
     if (try_rows<kNorm, kRes, 2>(a, dev, id, stream, &st)) return st;
-    if (try_rows<kNorm, kRes, 4>(a, dev, id, stream, &st)) return st;
+    if constexpr (kNorm)
+        if (try_rows<kNorm, kRes, 3>(a, dev, id, stream, &st)) return st;
+    if constexpr (!kRes)
+        if (try_rows<kNorm, kRes, 4>(a, dev, id, stream, &st)) return st;
     if constexpr (!kNorm)
         if (try_rows<kNorm, kRes, 8>(a, dev, id, stream, &st)) return st;
     // CTAs per SM by the row's KB of shared memory
@@ -417,7 +440,8 @@ nvfp4_status launch_rows(const RowArgs& a, void* stream) {
     const int64_t bytes = static_cast<int64_t>(a.cols) * (kNorm ? 4 : 2);
     if (bytes <= kLongSmem) {
         const int smem = static_cast<int>((bytes + 1023) / 1024 * 1024);
-        return launch(row_int8_long_kernel<kNorm, kRes, true>, staged[id][smem / 1024], kLongThreads, smem, a, dev,
+        return launch(row_int8_long_kernel<kNorm, kRes, true>, staged[id][smem / 1024],
+                      smem > kHalfSmem ? kLongThreads : kLongThreads / 2, smem, a, dev,
                       stream);
     }
     return launch(row_int8_long_kernel<kNorm, kRes, false>, unstaged[id], kLongThreads, 0, a, dev, stream);

@@ -168,7 +168,34 @@ def test_norm_shapes(rows, cols, pad, residual, offset):
     assert_norm(x, res, w, offset, 1e-6, q, out)
 
 
-@pytest.mark.parametrize("cols", [5120, 33024])
+# the last row length of each kernel and the first of the next, several rows a CTA
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("rows,cols,pad", [(300, 16384, 0), (299, 16400, 8), (330, 17408, 0), (150, 24576, 16),
+                                           (151, 24592, 0), (300, 28672, 0), (155, 28688, 0), (149, 32768, 8),
+                                           (320, 32784, 0), (149, 51200, 0), (160, 51216, 0)])
+def test_norm_long_rows(rows, cols, pad, residual):
+    x, res, w = norm_inputs(rows, cols, residual, pad, 1.0, seed=rows + cols)
+    q, out = nv.add_rms_norm_int8(x, w, residual=res, weight_offset=1.0)
+    torch.cuda.synchronize()
+    some = torch.tensor([0, 1, 2, 147, 148, rows - 2, rows - 1], device=DEV)
+    assert_norm(x[some], None if res is None else res[some], w, 1.0, 1e-6,
+                nv.Int8Tensor(q.codes[some], q.scale[some]), None if res is None else out[some])
+    # and every row as if it were alone: the same codes, the same scale
+    again, out2 = nv.add_rms_norm_int8(x[3:4], w, residual=None if res is None else res[3:4], weight_offset=1.0)
+    assert torch.equal(again.codes[0], q.codes[3]) and torch.equal(again.scale[0], q.scale[3])
+
+
+@pytest.mark.parametrize("rows,cols", [(160, 40976), (299, 57344), (160, 57360), (149, 102400), (3, 102416)])
+def test_quantize_long_rows(rows, cols):
+    x = activations(rows, cols, seed=rows)
+    codes, scale = nv.int8_quantize(x)
+    torch.cuda.synchronize()
+    some = torch.tensor([0, 1, rows // 2, rows - 1], device=DEV)
+    want_c, want_s = ref.quantize(f32(x[some]))
+    assert same(codes[some].cpu(), want_c) and same(f32(scale[some]), want_s)
+
+
+@pytest.mark.parametrize("cols", [5120, 17408, 33024])
 @pytest.mark.parametrize("where", ["residual", "x"])
 def test_norm_in_place(where, cols):
     x, res, w = norm_inputs(40, cols, True, 0, 0.0, seed=5)
