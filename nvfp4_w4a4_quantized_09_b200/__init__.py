@@ -613,7 +613,7 @@ def _empty(*shape, dtype, device, stream):
     running, and it is kept from reuse until the current stream is done with
     it as well."""
     if stream is None:
-        return torch.empty(*shape, dtype=dtype, device=device)
+        return _torch_empty(*shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         t = torch.empty(*shape, dtype=dtype, device=device)
     t.record_stream(torch.cuda.current_stream(device))
@@ -643,15 +643,27 @@ def _check_row_scale(t, name: str, rows: int):
 # by its handle; and a single row's stride, which torch may report as anything,
 # is given as the row's length rounded up to 8.
 _BF16, _I8, _F32 = torch.bfloat16, torch.int8, torch.float32
-_current_device = torch.cuda.current_device
+_Tensor, _torch_empty = torch.Tensor, torch.empty
+# asked only once a CUDA tensor is there, so CUDA is up
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _bf16_rows(x, name: str):
+    """Rows, columns and row stride of a BF16 matrix with unit column stride."""
+    if not isinstance(x, _Tensor) or x.dtype is not _BF16 or x.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D bfloat16 tensor")
+    rows, cols = x.shape
+    ld, step = x.stride()
+    if step != 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    return rows, cols, ld if rows > 1 else (cols + 7) // 8 * 8
 
 
 def int8_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
                   scale: Optional[torch.Tensor] = None, stream=None):
     """int8 codes [rows, cols] and FP32 scales [rows] of a BF16 matrix:
     codes = RNE(x * (127 / max|row|)), scale = max|row| / 127."""
-    _check_bf16_matrix(x, "x")
-    rows, cols = x.shape
+    rows, cols, ld = _bf16_rows(x, "x")
     dev = x.get_device()
     same = dev >= 0 and dev == _current_device()
     if codes is not None:
@@ -667,8 +679,7 @@ def int8_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
     if scale is None:
         scale = _empty(rows, dtype=_F32, device=x.device, stream=stream)
     st = _lib.lib().nvfp4_int8_quantize(
-        x.data_ptr(), rows, cols, x.stride(0) if rows > 1 else (cols + 7) // 8 * 8, codes.data_ptr(),
-        scale.data_ptr(), _stream_handle(dev, stream))
+        x.data_ptr(), rows, cols, ld, codes.data_ptr(), scale.data_ptr(), _stream_handle(dev, stream))
     if st:
         raise Nvfp4Error("nvfp4_int8_quantize", st)
     return codes, scale
@@ -689,18 +700,16 @@ def add_rms_norm_int8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[
     pass: r = x + residual, v = r * (weight + weight_offset) / sqrt(mean(r^2) + eps),
     quantized per row.  Returns (Int8Tensor of v, r in BF16); the second is
     None without a residual.  residual_out may be residual or x (in place)."""
-    _check_bf16_matrix(x, "x")
-    shape = x.shape
-    rows, cols = shape
+    rows, cols, ldx = _bf16_rows(x, "x")
     if not isinstance(weight, torch.Tensor) or weight.dtype is not _BF16 \
             or weight.shape != (cols,) or not weight.is_contiguous():
         raise ValueError(f"weight must be a contiguous bfloat16 tensor of {cols} elements")
     dev = x.get_device()
     same = dev >= 0 and dev == _current_device() and weight.get_device() == dev
     if residual is not None:
-        _check_bf16_matrix(residual, "residual")
-        if residual.shape != shape:
-            raise ValueError(f"residual must have shape {tuple(shape)}, got {tuple(residual.shape)}")
+        rows_r, cols_r, ldr = _bf16_rows(residual, "residual")
+        if rows_r != rows or cols_r != cols:
+            raise ValueError(f"residual must have shape {(rows, cols)}, got {(rows_r, cols_r)}")
         same = same and residual.get_device() == dev
         if residual_out is not None:
             _check_out_matrix(residual_out, "residual_out", _BF16, rows, cols)
@@ -721,16 +730,18 @@ def add_rms_norm_int8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[
         codes = _empty(rows, cols, dtype=_I8, device=device, stream=stream)
     if scale is None:
         scale = _empty(rows, dtype=_F32, device=device, stream=stream)
-    one = (cols + 7) // 8 * 8 if rows <= 1 else 0
-    r = ldr = out = ldo = 0
+    r = out = ldo = 0
     if residual is not None:
         if residual_out is None:
-            residual_out = _empty(rows, cols, dtype=_BF16, device=device, stream=stream)
-        r, ldr = residual.data_ptr(), one or residual.stride(0)
-        out, ldo = residual_out.data_ptr(), one or residual_out.stride(0)
+            residual_out, ldo = _empty(rows, cols, dtype=_BF16, device=device, stream=stream), (cols + 7) // 8 * 8
+        else:
+            _, _, ldo = _bf16_rows(residual_out, "residual_out")
+        r, out = residual.data_ptr(), residual_out.data_ptr()
+    else:
+        ldr = 0
     st = _lib.lib().nvfp4_add_rms_norm_int8(
-        x.data_ptr(), one or x.stride(0), r, ldr, weight.data_ptr(), weight_offset, eps, rows, cols,
-        out, ldo, codes.data_ptr(), scale.data_ptr(), _stream_handle(dev, stream))
+        x.data_ptr(), ldx, r, ldr, weight.data_ptr(), weight_offset, eps, rows, cols, out, ldo,
+        codes.data_ptr(), scale.data_ptr(), _stream_handle(dev, stream))
     if st:
         raise Nvfp4Error("nvfp4_add_rms_norm_int8", st)
     return Int8Tensor(codes, scale), residual_out
