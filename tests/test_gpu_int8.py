@@ -395,6 +395,20 @@ def test_gemm_shared_rows_on_two_streams_and_captured():
     assert all(torch.equal(x, want[0]) and torch.equal(y, want[1]) for x, y in got)
 
 
+@pytest.mark.parametrize("M,N,K", [(5, 300, 8192), (100, 2048, 17408), (300, 517, 17424)])
+def test_gemm_shared_rows_behind_a_long_kernel_and_with_non_finite_scales(M, N, K):
+    a, w = gemm_inputs(M, N, K, seed=3)
+    want = nv.int8_gemm(a, w)
+    torch.cuda.synchronize()
+    a.scale[M - 1], w.scale[N - 1] = float("nan"), float("inf")
+    torch.cuda._sleep(3_000_000_000)                 # about 1.5 s
+    y = nv.int8_gemm(a, w)
+    torch.cuda.synchronize()
+    assert nv.last_device_status() == 0
+    assert bool(y[M - 1].isnan().all()) and not bool(y[:M - 1, N - 1].isfinite().any())
+    assert torch.equal(y[:M - 1, :N - 1], want[:M - 1, :N - 1])
+
+
 @pytest.mark.parametrize("M", [1, 5, 129, 300])
 @pytest.mark.parametrize("fill", [(-128, -128), (127, -128), (127, 127)])
 def test_gemm_largest_sums(M, fill):
