@@ -21,6 +21,7 @@ mlp and the weight file take them too.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 from dataclasses import dataclass
@@ -124,6 +125,30 @@ def _check_devices(**tensors) -> torch.device:
     return dev
 
 
+# Every call takes `stream`: its kernels run there.  The caller's tensors have to
+# be ready on it and to outlive the work, as for any kernel on another stream;
+# what a call allocates by itself, outputs and the intermediates it drops before
+# it returns, comes from these two.
+_torch_empty = torch.empty
+
+
+def _on(stream):
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _empty(*shape, dtype, device, stream):
+    """torch.empty for a kernel on `stream`: with an explicit stream the memory
+    is that stream's, so that no earlier use of it on another one can still be
+    running, and it is kept from reuse until the current stream is done with
+    it as well."""
+    if stream is None:
+        return _torch_empty(*shape, dtype=dtype, device=device)
+    with _on(stream):
+        t = _torch_empty(*shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 _workspaces = {}
 
 
@@ -166,8 +191,10 @@ def global_scale(x: torch.Tensor, g_out: Optional[torch.Tensor] = None,
     if workspace is not None:
         _check_packed(workspace, "workspace", min_bytes=_lib.GLOBAL_SCALE_WORKSPACE_BYTES)
     dev = _check_devices(x=x, g_out=g_out, amax_out=amax_out, workspace=workspace)
-    g_out = torch.empty(1, dtype=torch.float32, device=dev) if g_out is None else g_out
-    amax_out = torch.empty(1, dtype=torch.float32, device=dev) if amax_out is None else amax_out
+    if g_out is None:
+        g_out = _empty(1, dtype=torch.float32, device=dev, stream=stream)
+    if amax_out is None:
+        amax_out = _empty(1, dtype=torch.float32, device=dev, stream=stream)
     ws = _workspace(dev, stream) if workspace is None else workspace
     rows, cols = x.shape
     _lib.check("nvfp4_global_scale", _lib.lib().nvfp4_global_scale(
@@ -200,9 +227,9 @@ def quantize(x: torch.Tensor, g: torch.Tensor, layout: int = SF_TCGEN05,
         _check_packed(sf, "sf", min_bytes=_sf_bytes_cached(rows, cols, layout))
     dev = _check_devices(x=x, g=g, codes=codes, sf=sf)
     if codes is None:
-        codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device=dev)
+        codes = _empty(rows, cols // 2, dtype=torch.uint8, device=dev, stream=stream)
     if sf is None:
-        sf = torch.empty(sf_bytes(rows, cols, layout), dtype=torch.uint8, device=dev)
+        sf = _empty(sf_bytes(rows, cols, layout), dtype=torch.uint8, device=dev, stream=stream)
     _lib.check("nvfp4_quantize", _lib.lib().nvfp4_quantize(
         _ptr(x), rows, cols, x.stride(0), _ptr(g), _ptr(codes), _ptr(sf), layout, _stream(stream)))
     return codes, sf
@@ -246,7 +273,7 @@ def gemm(a: QuantizedTensor, w: QuantizedTensor, y: Optional[torch.Tensor] = Non
     dev = _check_devices(a_codes=a.codes, a_sf=a.sf, a_g=a.g, w_codes=w.codes, w_sf=w.sf, w_g=w.g,
                          y=y)
     if y is None:
-        y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+        y = _empty(M, N, dtype=torch.bfloat16, device=dev, stream=stream)
     _lib.check("nvfp4_gemm", _lib.lib().nvfp4_gemm(
         _ptr(a.codes), _ptr(a.sf), _ptr(a.g), _ptr(w.codes), _ptr(w.sf), _ptr(w.g),
         _ptr(y), y.stride(0), M, N, K, _stream(stream)))
@@ -273,9 +300,9 @@ class FusedWeight:
             _check_bf16_matrix(w, f"weights[{i}]")
         cols = weights[0].shape[1]
         total = sum(w.shape[0] for w in weights)
-        dev = weights[0].device
-        codes = torch.empty(total, cols // 2, dtype=torch.uint8, device=dev)
-        sf = torch.empty(sf_bytes(total, cols, SF_TCGEN05), dtype=torch.uint8, device=dev)
+        dev = _check_devices(**{f"weights[{i}]": w for i, w in enumerate(weights)})
+        codes = _empty(total, cols // 2, dtype=torch.uint8, device=dev, stream=stream)
+        sf = _empty(sf_bytes(total, cols, SF_TCGEN05), dtype=torch.uint8, device=dev, stream=stream)
         gs, off = [], 0
         for w in weights:
             if w.shape[1] != cols:
@@ -311,8 +338,10 @@ def harmonize(w: "FusedWeight", layout: int = SF_TCGEN05, stream=None) -> Quanti
     segs = w.segments()
     _check_segments(segs, w.rows)
     dev = _check_devices(w_sf=w.sf, **{f"g[{i}]": g for i, (_, _, g) in enumerate(segs)})
-    sf = w.sf.clone()
-    g_c = torch.empty(1, dtype=torch.float32, device=dev)
+    sf = _empty(*w.sf.shape, dtype=torch.uint8, device=dev, stream=stream)
+    with _on(stream):
+        sf.copy_(w.sf)
+    g_c = _empty(1, dtype=torch.float32, device=dev, stream=stream)
     _lib.check("nvfp4_harmonize_scales", _lib.lib().nvfp4_harmonize_scales(
         _ptr(sf), w.cols, _segment_array(segs), len(segs), layout, _ptr(g_c), _stream(stream)))
     return QuantizedTensor(w.codes, sf, g_c, w.rows, w.cols, layout)
@@ -370,7 +399,7 @@ def fused_gemm(a: QuantizedTensor, w_codes: torch.Tensor, w_sf: torch.Tensor,
                          **{f"segments[{i}] g": g for i, (_, _, g) in enumerate(segments)}, **params)
     arr = _segment_array(segments)
     if y is None:
-        y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+        y = _empty(M, N, dtype=torch.bfloat16, device=dev, stream=stream)
     if acts is None:
         _lib.check("nvfp4_fused_gemm", _lib.lib().nvfp4_fused_gemm(
             _ptr(a.codes), _ptr(a.sf), _ptr(a.g), _ptr(w_codes), _ptr(w_sf), arr, nseg,
@@ -523,8 +552,8 @@ def gemm_silu_mul(a: QuantizedTensor, w_interleaved: QuantizedTensor,
                          w_sf=w_interleaved.sf, w_g=w_interleaved.g, h=h)
     if h is None:
         h = _empty(M, F, dtype=torch.bfloat16, device=dev, stream=stream)
-    g_h = torch.empty(1, dtype=torch.float32, device=dev)
-    amax_h = torch.empty(1, dtype=torch.float32, device=dev)
+    g_h = _empty(1, dtype=torch.float32, device=dev, stream=stream)
+    amax_h = _empty(1, dtype=torch.float32, device=dev, stream=stream)
     _lib.check("nvfp4_gemm_silu_mul", _lib.lib().nvfp4_gemm_silu_mul(
         _ptr(a.codes), _ptr(a.sf), _ptr(a.g), _ptr(w_interleaved.codes), _ptr(w_interleaved.sf),
         _ptr(w_interleaved.g), _ptr(h), h.stride(0), M, F, K, _ptr(_workspace(dev, stream)),
@@ -558,7 +587,7 @@ def kv_scale(calibration: torch.Tensor, stream=None) -> torch.Tensor:
     """Calibrated per-tensor FP8 KV-cache scale fl32(amax / 448) of a BF16
     calibration tensor (device FP32, 1 element)."""
     _, amax = global_scale(calibration, stream=stream)
-    s = torch.empty(1, dtype=torch.float32, device=calibration.device)
+    s = _empty(1, dtype=torch.float32, device=calibration.device, stream=stream)
     _lib.check("nvfp4_kv_scale_from_amax",
                _lib.lib().nvfp4_kv_scale_from_amax(_ptr(amax), _ptr(s), _stream(stream)))
     return s
@@ -574,7 +603,7 @@ def kv_quantize(x: torch.Tensor, scale: torch.Tensor, out: Optional[torch.Tensor
         _check_out_matrix(out, "out", torch.uint8, rows, cols)
     dev = _check_devices(x=x, scale=scale, out=out)
     if out is None:
-        out = torch.empty(rows, cols, dtype=torch.uint8, device=dev)
+        out = _empty(rows, cols, dtype=torch.uint8, device=dev, stream=stream)
     _lib.check("nvfp4_kv_quantize_e4m3", _lib.lib().nvfp4_kv_quantize_e4m3(
         _ptr(x), rows, cols, x.stride(0), _ptr(scale), _ptr(out), out.stride(0), _stream(stream)))
     return out
@@ -607,19 +636,6 @@ class Int8Tensor:
         return cls(torch.cat([t.codes for t in tensors]), torch.cat([t.scale for t in tensors]))
 
 
-def _empty(*shape, dtype, device, stream):
-    """torch.empty for a kernel on `stream`: with an explicit stream the memory
-    is that stream's, so that no earlier use of it on another one can still be
-    running, and it is kept from reuse until the current stream is done with
-    it as well."""
-    if stream is None:
-        return _torch_empty(*shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(*shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(device))
-    return t
-
-
 def _stream_handle(index: int, stream) -> int:
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
@@ -643,7 +659,7 @@ def _check_row_scale(t, name: str, rows: int):
 # by its handle; and a single row's stride, which torch may report as anything,
 # is given as the row's length rounded up to 8.
 _BF16, _I8, _F32 = torch.bfloat16, torch.int8, torch.float32
-_Tensor, _torch_empty = torch.Tensor, torch.empty
+_Tensor = torch.Tensor
 # asked only once a CUDA tensor is there, so CUDA is up
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 

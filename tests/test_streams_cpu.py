@@ -1,0 +1,115 @@
+"""Which stream a call's memory belongs to, without a GPU.
+
+With an explicit stream, everything a call allocates by itself has to come from
+that stream's memory: an intermediate that the call drops on return could
+otherwise be handed out again on the caller's stream while kernels on the other
+one still read or write it.  The library is replaced by one that computes
+nothing; what is checked is each allocation and the stream it names."""
+import contextlib
+
+import pytest
+import torch
+
+import nvfp4_w4a4_quantized_09_b200 as nv
+
+BF = torch.bfloat16
+X = torch.zeros(8, 256, dtype=BF)
+
+
+class Stream:
+    cuda_stream = 0x50
+
+
+S = Stream()
+
+
+class NoKernels:
+    """The library's entry points, none of which does anything but sf_bytes."""
+
+    def __init__(self, real):
+        self.real = real
+
+    def __getattr__(self, name):
+        return getattr(self.real, name) if name == "nvfp4_sf_bytes" else lambda *args: 0
+
+
+def q4(rows, cols):
+    return nv.QuantizedTensor(torch.zeros(rows, cols // 2, dtype=torch.uint8),
+                              torch.zeros(nv.sf_bytes(rows, cols), dtype=torch.uint8), torch.ones(1), rows, cols)
+
+
+def q8(rows, cols):
+    return nv.Int8Tensor(torch.zeros(rows, cols, dtype=torch.int8), torch.ones(rows))
+
+
+def fused(cols=256):
+    w = q4(96, cols)
+    return nv.FusedWeight(w.codes, w.sf, [torch.ones(1), torch.ones(1)], [64, 32], cols)
+
+
+CALLS = {
+    "global_scale": lambda: nv.global_scale(X, stream=S),
+    "quantize": lambda: nv.quantize(X, torch.ones(1), stream=S),
+    "quantize_tensor": lambda: nv.quantize_tensor(X, stream=S),
+    "gemm": lambda: nv.gemm(q4(8, 256), q4(64, 256), stream=S),
+    "fused_gemm": lambda: nv.fused_gemm(q4(8, 256), fused().codes, fused().sf, fused().segments(), stream=S),
+    "from_modules": lambda: nv.FusedWeight.from_modules([X, X], stream=S),
+    "harmonize": lambda: nv.harmonize(fused(), stream=S),
+    "silu_mul": lambda: nv.silu_mul(X, stream=S),
+    "gemm_silu_mul": lambda: nv.gemm_silu_mul(q4(300, 256), q4(512, 256), stream=S),
+    "kv_scale": lambda: nv.kv_scale(X, stream=S),
+    "kv_quantize": lambda: nv.kv_quantize(X, torch.ones(1), stream=S),
+    "int8_quantize": lambda: nv.int8_quantize(X, stream=S),
+    "add_rms_norm_int8": lambda: nv.add_rms_norm_int8(X, X[0], residual=X, stream=S),
+    "int8_gemm": lambda: nv.int8_gemm(q8(8, 256), q8(63, 256), stream=S),
+    "linear, 4 bits": lambda: nv.linear(X, q4(64, 256), stream=S),
+    "linear, fused": lambda: nv.linear(X, fused(), stream=S),
+    "linear, 8 bits": lambda: nv.linear(X, q8(64, 256), stream=S),
+    "mlp, 4 bits": lambda: nv.mlp(X, q4(512, 256), q4(256, 256), stream=S),
+    "mlp, 4 then 8 bits": lambda: nv.mlp(X, q4(512, 256), q8(256, 256), stream=S),
+    "mlp, 8 then 4 bits": lambda: nv.mlp(X, q8(512, 256), q4(256, 256), stream=S),
+    "mlp, interleaved": lambda: nv.mlp(X, q4(512, 256), q4(256, 256), stream=S, interleaved=True),
+    "mlp, interleaved then 8 bits": lambda: nv.mlp(X, q4(512, 256), q8(256, 256), stream=S, interleaved=True),
+}
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_a_call_allocates_on_its_stream_alone(monkeypatch, call):
+    real = {name: getattr(torch, name) for name in ("empty", "empty_strided", "empty_like", "zeros")}
+    streams, elsewhere = [], []
+
+    def empty(*shape, dtype, device, stream):
+        streams.append(stream)
+        return real["empty"](*shape, dtype=dtype)
+
+    def other(name):
+        def allocate(*args, **kwargs):
+            elsewhere.append((name, args))
+            return real[name](*args, **kwargs)
+        return allocate
+
+    run = CALLS[call]
+    workspace, lib = torch.zeros(4096, dtype=torch.uint8), NoKernels(nv._lib.lib())
+    monkeypatch.setattr(nv, "_check_devices", lambda **tensors: torch.device("cpu"))
+    monkeypatch.setattr(nv, "_workspace", lambda device, stream=None: workspace)
+    monkeypatch.setattr(nv._lib, "lib", lambda: lib)
+    monkeypatch.setattr(nv, "_empty", empty)
+    monkeypatch.setattr(nv, "_on", lambda stream: contextlib.nullcontext(), raising=False)
+    inputs = {"q4": q4, "q8": q8, "fused": fused}
+    for name, make in inputs.items():        # made before the allocations are watched
+        made = {}
+
+        def once(*args, make=make, made=made):
+            if args not in made:
+                made[args] = make(*args)
+            return made[args]
+        monkeypatch.setitem(globals(), name, once)
+    run()
+    streams.clear()
+    for name in real:
+        monkeypatch.setattr(torch, name, other(name))
+    clone = torch.Tensor.clone
+    monkeypatch.setattr(torch.Tensor, "clone", lambda t, **kw: elsewhere.append(("clone", t.shape)) or clone(t, **kw))
+    run()
+    assert not elsewhere
+    assert streams and all(s is S for s in streams)
