@@ -155,14 +155,19 @@ _workspaces = {}
 def _workspace(device: torch.device, stream=None) -> torch.Tensor:
     """Zero-initialised global-scale workspace, one per (device, stream): each
     call leaves it zeroed again, and calls on one stream run in order, so
-    calls on different streams never share one."""
-    idx = device.index if device.index is not None else torch.cuda.current_device()
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    key = (idx, s.cuda_stream)
-    ws = _workspaces.get(key)
-    if ws is None:
-        ws = torch.zeros(_lib.GLOBAL_SCALE_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
-        _workspaces[key] = ws
+    calls on different streams never share one.  It is zeroed on the stream
+    that uses it.  A captured call gets its own, zeroed by a node of the graph:
+    graphs captured on one stream may be replayed on several at once."""
+    with _on(stream):
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros(_lib.GLOBAL_SCALE_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+        idx = device.index if device.index is not None else torch.cuda.current_device()
+        s = stream if stream is not None else torch.cuda.current_stream(device)
+        key = (idx, s.cuda_stream)
+        ws = _workspaces.get(key)
+        if ws is None:
+            ws = torch.zeros(_lib.GLOBAL_SCALE_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+            _workspaces[key] = ws
     return ws
 
 
@@ -554,9 +559,10 @@ def gemm_silu_mul(a: QuantizedTensor, w_interleaved: QuantizedTensor,
         h = _empty(M, F, dtype=torch.bfloat16, device=dev, stream=stream)
     g_h = _empty(1, dtype=torch.float32, device=dev, stream=stream)
     amax_h = _empty(1, dtype=torch.float32, device=dev, stream=stream)
+    ws = _workspace(dev, stream)
     _lib.check("nvfp4_gemm_silu_mul", _lib.lib().nvfp4_gemm_silu_mul(
         _ptr(a.codes), _ptr(a.sf), _ptr(a.g), _ptr(w_interleaved.codes), _ptr(w_interleaved.sf),
-        _ptr(w_interleaved.g), _ptr(h), h.stride(0), M, F, K, _ptr(_workspace(dev, stream)),
+        _ptr(w_interleaved.g), _ptr(h), h.stride(0), M, F, K, _ptr(ws),
         _ptr(g_h), _ptr(amax_h), _stream(stream)))
     return h, g_h, amax_h
 

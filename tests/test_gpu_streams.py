@@ -74,3 +74,43 @@ def test_weights_quantized_on_another_stream():
         assert torch.equal(got_h.sf, want_h.sf) and torch.equal(got_h.g, want_h.g)
         assert torch.equal(got_kv, want_kv)
         del kept
+
+
+def test_a_fresh_streams_workspace_is_zeroed_before_its_first_use():
+    # the current stream is busy, and the memory a new workspace may get is dirty
+    x = synth.student_t_activations(64, H, seed=1, device=DEV)
+    want = nv.quantize_tensor(x)
+    for _ in range(3):
+        dirty = [torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV) for n in (64, 256, 512) for _ in range(8)]
+        torch.cuda.synchronize()
+        del dirty
+        s = torch.cuda.Stream()
+        torch.cuda._sleep(100_000_000)
+        got = nv.quantize_tensor(x, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(got.g, want.g) and torch.equal(got.codes, want.codes)
+
+
+@pytest.mark.parametrize("first,second", [("4", "8"), ("4", "4"), ("interleaved", "8"), ("interleaved", "4")])
+def test_two_captured_mlps_replayed_at_once(first, second):
+    M = 300
+    w = weights()
+    kwargs = {"interleaved": first == "interleaved"}
+    xs = [synth.student_t_activations(M, H, seed=i, device=DEV) * (1 + 30 * i) for i in range(2)]
+    want = [nv.mlp(x, w[first][0], w[second][1], **kwargs) for x in xs]
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for x in xs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append([nv.mlp(x, w[first][0], w[second][1], **kwargs) for _ in range(3)])
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(50):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert nv.last_device_status() == 0
+    for outs, right in zip(got, want):
+        assert all(torch.equal(o, right) for o in outs)

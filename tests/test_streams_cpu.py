@@ -113,3 +113,42 @@ def test_a_call_allocates_on_its_stream_alone(monkeypatch, call):
     run()
     assert not elsewhere
     assert streams and all(s is S for s in streams)
+
+
+def watch_zeros(monkeypatch, capturing):
+    """Every torch.zeros call with the stream it is made on (None: the current)."""
+    zeros, on, made = torch.zeros, [None], []
+
+    @contextlib.contextmanager
+    def enter(stream):
+        on.append(stream if stream is not None else on[-1])
+        yield
+        on.pop()
+
+    def make(*args, **kwargs):
+        made.append(on[-1])
+        return zeros(*args, dtype=kwargs["dtype"])
+
+    monkeypatch.setattr(nv, "_on", enter, raising=False)
+    monkeypatch.setattr(nv, "_workspaces", {})
+    monkeypatch.setattr(torch, "zeros", make)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream())
+    return made
+
+
+def test_a_workspace_is_zeroed_on_its_stream_and_kept(monkeypatch):
+    made = watch_zeros(monkeypatch, capturing=False)
+    dev = torch.device("cuda", 0)
+    ws = nv._workspace(dev, S)
+    assert made == [S]                       # ordered before the kernel that reads it
+    assert nv._workspace(dev, S) is ws and made == [S]
+
+
+@pytest.mark.parametrize("stream", [None, S])
+def test_captured_calls_share_no_workspace(monkeypatch, stream):
+    made = watch_zeros(monkeypatch, capturing=True)
+    dev = torch.device("cuda", 0)
+    a, b = nv._workspace(dev, stream), nv._workspace(dev, stream)
+    assert a.data_ptr() != b.data_ptr() and made == [stream] * 2
+    assert not nv._workspaces                # nor does a later call outside the graph use them
