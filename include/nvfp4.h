@@ -199,7 +199,8 @@ nvfp4_status nvfp4_quantize_slice(const void* x, int64_t rows, int64_t cols, int
  *   a_codes [M, K/2], w_codes [N, K/2]  (device, packed as above, K-major)
  *   a_sf, w_sf  (device) block scales in NVFP4_SF_TCGEN05 layout
  *   a_g, w_g    (device) FP32 global scales
- *   y [M, N] BF16 (device), row stride ldy elements
+ *   y [M, N] BF16 (device), row stride ldy elements; columns beyond N are not
+ *     written
  * Weights are [N, K] (the nn.Linear convention) and are quantized with
  * nvfp4_quantize like activations.  No bias.
  * Requirements: K % 32 == 0, K >= 32; ldy >= N, ldy % 8 == 0; all pointers

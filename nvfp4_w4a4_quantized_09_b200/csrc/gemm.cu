@@ -965,6 +965,18 @@ nvf4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 uint32_t o[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+                if (n0 + 32 > args.N && (args.N & 7) != 0) {                   // warp-uniform
+                    // TMA stores whole 16-byte pieces of a row: columns that
+                    // end inside one are stored from here, or up to seven
+                    // columns of y beyond N would be written over
+                    if (m0 + lane < args.M) {
+                        uint16_t* yp = args.y + static_cast<int64_t>(m0 + lane) * args.ldy + n0;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (n0 + j < args.N) yp[j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
+                    }
+                    continue;
+                }
                 // the previous chunk's store has finished reading the buffer
                 if (ch > 0) {
                     if (lane == 0) bulk_wait_read_all();
