@@ -441,17 +441,21 @@ class HostLinearScratch:
     """Device scratch of linear_host for one (M, K, N): the activation copy,
     its codes, scales, global scale and amax, the global-scale workspace and
     the output before its copy back.  Reuse it across calls of that shape on
-    one stream (its workspace is left zeroed by every call)."""
+    one stream (its workspace is left zeroed by every call): `stream`, or the
+    current one at its making."""
 
-    def __init__(self, M: int, K: int, N: int, device):
+    def __init__(self, M: int, K: int, N: int, device, stream=None):
         self.shape = (int(M), int(K), int(N))
-        self.x = torch.empty(M, K, dtype=torch.bfloat16, device=device)
-        self.codes = torch.empty(M, K // 2, dtype=torch.uint8, device=device)
-        self.sf = torch.empty(sf_bytes(M, K), dtype=torch.uint8, device=device)
-        self.g = torch.empty(1, dtype=torch.float32, device=device)
-        self.amax = torch.empty(1, dtype=torch.float32, device=device)
-        self.workspace = torch.zeros(_lib.GLOBAL_SCALE_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
-        self.y = torch.empty(M, N, dtype=torch.bfloat16, device=device)
+        u8, f32, bf16 = torch.uint8, torch.float32, torch.bfloat16
+        self.x = _empty(M, K, dtype=bf16, device=device, stream=stream)
+        self.codes = _empty(M, K // 2, dtype=u8, device=device, stream=stream)
+        self.sf = _empty(sf_bytes(M, K), dtype=u8, device=device, stream=stream)
+        self.g = _empty(1, dtype=f32, device=device, stream=stream)
+        self.amax = _empty(1, dtype=f32, device=device, stream=stream)
+        self.workspace = _empty(_lib.GLOBAL_SCALE_WORKSPACE_BYTES, dtype=u8, device=device, stream=stream)
+        with _on(stream):
+            self.workspace.zero_()
+        self.y = _empty(M, N, dtype=bf16, device=device, stream=stream)
 
 
 def linear_host(x_host: torch.Tensor, w, y_host: Optional[torch.Tensor] = None,
@@ -466,7 +470,9 @@ def linear_host(x_host: torch.Tensor, w, y_host: Optional[torch.Tensor] = None,
     out on that stream in row slices while the GEMM proceeds, and consecutive
     calls overlap one call's copy out with the next one's copy in: y_host is
     ready once copy_stream has passed the call.  The copies are asynchronous
-    when the host tensors are page-locked."""
+    when the host tensors are page-locked, and the host tensors have to outlive
+    them.  Without `scratch` the call makes its own, which both streams are
+    done with before its memory is used again."""
     if not isinstance(x_host, torch.Tensor) or x_host.dtype != torch.bfloat16 or x_host.dim() != 2 \
             or x_host.is_cuda or not x_host.is_contiguous():
         raise ValueError("x_host must be a contiguous 2-D bfloat16 host tensor")
@@ -489,13 +495,16 @@ def linear_host(x_host: torch.Tensor, w, y_host: Optional[torch.Tensor] = None,
     elif (not isinstance(y_host, torch.Tensor) or y_host.dtype != torch.bfloat16 or y_host.is_cuda
           or y_host.shape != (M, N) or not y_host.is_contiguous()):
         raise ValueError(f"y_host must be a contiguous bfloat16 host tensor of shape ({M}, {N})")
+    own = False
     if scratch is None:
-        scratch = HostLinearScratch(M, K, N, w.codes.device)
+        scratch, own = HostLinearScratch(M, K, N, w.codes.device, stream), True
     elif scratch.shape != (M, K, N):
         raise ValueError(f"scratch is for {scratch.shape}, the call needs {(M, K, N)}")
     _check_devices(w_codes=w.codes, w_sf=w.sf, x=scratch.x, codes=scratch.codes, sf=scratch.sf,
                    g=scratch.g, workspace=scratch.workspace, y=scratch.y,
                    **{f"segments[{i}] g": g for i, (_, _, g) in enumerate(segments)})
+    if own and copy_stream is not None:
+        scratch.y.record_stream(copy_stream)
     args = (_ptr(x_host), M, K, _ptr(w.codes), _ptr(w.sf), _segment_array(segments), len(segments),
             _ptr(y_host), _ptr(scratch.x), _ptr(scratch.codes), _ptr(scratch.sf), _ptr(scratch.g),
             _ptr(scratch.amax), _ptr(scratch.workspace), _ptr(scratch.y), _stream(stream))

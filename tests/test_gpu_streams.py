@@ -114,3 +114,30 @@ def test_two_captured_mlps_replayed_at_once(first, second):
     assert nv.last_device_status() == 0
     for outs, right in zip(got, want):
         assert all(torch.equal(o, right) for o in outs)
+
+
+@pytest.mark.parametrize("M", [5, 300, 5000])
+@pytest.mark.parametrize("overlap", [False, True])
+def test_host_call_without_a_scratch(M, overlap):
+    x = synth.student_t_activations(M, H, seed=1, device=DEV)
+    fw = nv.FusedWeight.from_modules([synth.gaussian_weights(n, H, 0.02, seed=n, device=DEV) for n in (256, 64)])
+    want = nv.linear(x, fw).cpu()
+    x_host = x.cpu().pin_memory()
+    y_hosts = [torch.empty(M, fw.rows, dtype=torch.bfloat16).pin_memory() for _ in range(3)]
+    s, c = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for kwargs in ({"stream": s}, {}):
+        if overlap:
+            kwargs["copy_stream"] = c
+        for y_host in y_hosts:
+            delay(kwargs.get("stream", torch.cuda.current_stream()))
+            delay(c)
+            nv.linear_host(x_host, fw, y_host, **kwargs)
+            kept = [torch.full((n,), 0x7F, dtype=torch.uint8, device=DEV)
+                    for n in (4, 256, 2 * M * fw.rows, 2 * M * H, M * H // 2, nv.sf_bytes(M, H)) for _ in range(3)]
+        torch.cuda.synchronize()
+        for y_host in y_hosts:
+            assert torch.equal(y_host, want)
+            y_host.zero_()
+        del kept
+    assert nv.last_device_status() == 0

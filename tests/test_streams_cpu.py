@@ -115,6 +115,40 @@ def test_a_call_allocates_on_its_stream_alone(monkeypatch, call):
     assert streams and all(s is S for s in streams)
 
 
+def test_a_scratch_made_by_the_call_belongs_to_both_streams(monkeypatch):
+    # the call drops it while both streams still work on it
+    class CopyStream:
+        cuda_stream = 0x60
+
+    streams, on, recorded, copy = [], [None], [], CopyStream()
+
+    @contextlib.contextmanager
+    def enter(stream):
+        on.append(stream)
+        yield
+        on.pop()
+
+    def empty(*shape, dtype, device, stream):
+        streams.append(stream)
+        return torch.ones(*shape, dtype=dtype)
+
+    zero = torch.Tensor.zero_
+    zeroed = []
+    w, lib = fused(), NoKernels(nv._lib.lib())
+    monkeypatch.setattr(nv, "_check_devices", lambda **tensors: torch.device("cpu"))
+    monkeypatch.setattr(nv._lib, "lib", lambda: lib)
+    monkeypatch.setattr(nv, "_empty", empty)
+    monkeypatch.setattr(nv, "_on", enter)
+    monkeypatch.setattr(torch.Tensor, "zero_", lambda t: zeroed.append((t.numel(), on[-1])) or zero(t))
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((tuple(t.shape), s)))
+    y_host = torch.empty(8, 96, dtype=BF)
+    nv.linear_host(X, w, y_host, stream=S)
+    assert len(streams) == 7 and all(s is S for s in streams) and not recorded
+    assert zeroed == [(nv._lib.GLOBAL_SCALE_WORKSPACE_BYTES, S)]
+    nv.linear_host(X, w, y_host, stream=S, copy_stream=copy)
+    assert recorded == [((8, 96), copy)]
+
+
 def watch_zeros(monkeypatch, capturing):
     """Every torch.zeros call with the stream it is made on (None: the current)."""
     zeros, on, made = torch.zeros, [None], []
