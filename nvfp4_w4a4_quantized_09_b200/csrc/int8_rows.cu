@@ -287,6 +287,10 @@ __global__ void __launch_bounds__(row_max_threads(kNorm, V), row_min_ctas(kNorm,
 // wrote.  Two CTAs of 512 threads share an SM where their rows fit, else one has
 // 1024 (norm 4096 x 32768: 188 us, 214 with 512; plain 3000 x 49152: 81 us with two
 // CTAs, 103 with one).  Beyond shared memory the row is read twice.
+// A thread's sum of squares is one chain of binary32 additions: at most 56 of
+// them in a row that fits on chip, so that the scale errs by 2^-18 at the most.
+// Rows read twice may have any length (a chain of 32768, 2^25 columns, erred by
+// 2.4e-4): their batches of 32 are added up in binary64.
 constexpr int kLongThreads = 1024;              // half of them where two CTAs share an SM
 constexpr int kHalfSmem = 112 * 1024;
 constexpr int kLongBatch = 4;
@@ -308,6 +312,7 @@ __global__ void __launch_bounds__(kLongThreads, 1) row_int8_long_kernel(const Ro
         const uint16_t* res = kRes ? a.residual + row * a.ldr : nullptr;
         uint16_t* out = kRes && a.residual_out ? a.residual_out + row * a.ldo : nullptr;
         float sum = 0.0f;
+        double total = 0.0;
         uint32_t top = 0;
         for (int v0 = threadIdx.x; v0 < vecs; v0 += threads * kLongBatch) {
             uint4 xv[kLongBatch], rv[kLongBatch];
@@ -342,7 +347,9 @@ __global__ void __launch_bounds__(kLongThreads, 1) row_int8_long_kernel(const Ro
                     if constexpr (kStaged) s_row[v] = xv[j];
                 }
             }
+            if constexpr (kNorm && !kStaged) total += static_cast<double>(sum), sum = 0.0f;
         }
+        if constexpr (kNorm && !kStaged) sum = static_cast<float>(total);
         if constexpr (!kNorm) top = top_bits(top);
         reduce_row<kNorm>(sum, top, s_red[buf], threads / 32);
         float mult;
