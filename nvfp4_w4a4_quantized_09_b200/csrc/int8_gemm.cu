@@ -631,13 +631,13 @@ void launch_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2], int 
 
 nvfp4_status launch_few(const Operands& o, const DeviceInfo& info, int* status, cudaStream_t stream) {
     using Kernel = void (*)(CUtensorMap, CUtensorMap, FewArgs);
-    static const Kernel kernels[3][4] = {
-        {int8_gemm_few_kernel<1, false, false>, int8_gemm_few_kernel<2, false, false>,
-         int8_gemm_few_kernel<4, false, false>, int8_gemm_few_kernel<8, false, false>},
-        {int8_gemm_few_kernel<1, true, false>, int8_gemm_few_kernel<2, true, false>,
-         int8_gemm_few_kernel<4, true, false>, int8_gemm_few_kernel<8, true, false>},
-        {int8_gemm_few_kernel<1, false, true>, int8_gemm_few_kernel<2, false, true>,
-         int8_gemm_few_kernel<4, false, true>, int8_gemm_few_kernel<8, false, true>}};
+    static const Kernel whole[4] = {
+        int8_gemm_few_kernel<1, false, false>, int8_gemm_few_kernel<2, false, false>,
+        int8_gemm_few_kernel<4, false, false>, int8_gemm_few_kernel<8, false, false>};
+    static const Kernel shared[4] = {
+        int8_gemm_few_kernel<1, false, true>, int8_gemm_few_kernel<2, false, true>,
+        int8_gemm_few_kernel<4, false, true>, int8_gemm_few_kernel<8, false, true>};
+    static const Kernel swapped = int8_gemm_few_kernel<kSwapSteps, true, false>;
     static PerDeviceOnce once;
     static int resident[kMaxDevices][kMaxSplits + 1];     // clusters of 2, 4 and 8 CTAs that fit the device
     int dev = 0;
@@ -646,14 +646,14 @@ nvfp4_status launch_few(const Operands& o, const DeviceInfo& info, int* status, 
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
     st = once.run(dev, [&] {
-        for (const auto& row : kernels)
-            for (const Kernel k : row)
-                if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem) != cudaSuccess)
-                    return NVFP4_ERR_CUDA;
+        for (const Kernel k : {whole[0], whole[1], whole[2], whole[3], shared[0], shared[1], shared[2], shared[3],
+                               swapped})
+            if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem) != cudaSuccess)
+                return NVFP4_ERR_CUDA;
         for (int s = 2; s <= kMaxSplits; s *= 2) {
             launch_config(&cfg, attr, s, kFewThreads, kFewSmem, nullptr);
             cfg.gridDim = dim3(static_cast<unsigned>(info.sms / s * s), 1, 1);
-            if (cudaOccupancyMaxActiveClusters(&resident[dev][s], kernels[2][0], &cfg) != cudaSuccess)
+            if (cudaOccupancyMaxActiveClusters(&resident[dev][s], shared[0], &cfg) != cudaSuccess)
                 return NVFP4_ERR_CUDA;
         }
         return NVFP4_OK;
@@ -661,14 +661,14 @@ nvfp4_status launch_few(const Operands& o, const DeviceInfo& info, int* status, 
     if (st != NVFP4_OK) return st;
     FewArgs f = {};
     f.sa = o.sa, f.sw = o.sw, f.y = o.y, f.ldy = o.ldy, f.M = o.M, f.N = o.N, f.K = o.K;
+    f.k_steps = (o.K + kStepBytes - 1) / kStepBytes;
+    f.timeout_ns = kTimeoutNs;
+    f.status = status;
     // Channels as the MMA's rows: a long stream of few tokens (see the top of
     // int8_gemm_few.cuh), long enough for the power limit to show and to fill
     // rounds of 128-channel tiles.
     const bool swap = o.M <= kSwapTokens && o.N >= 224 * info.sms;
     f.nt = swap ? (o.M + 15) / 16 * 16 : (o.M + 7) / 8 * 8;
-    f.k_steps = (o.K + kStepBytes - 1) / kStepBytes;
-    f.timeout_ns = kTimeoutNs;
-    f.status = status;
     // Tile width and the split of K, by cycles.  Over all rounds of tiles an SM
     // spends on each k-step the larger of its MMAs (four of BN / 2, 56 at the
     // least or 44 with 64 rows, and 300 for a stage's handshake) and its feed
@@ -682,11 +682,14 @@ nvfp4_status launch_few(const Operands& o, const DeviceInfo& info, int* status, 
     int u = 0;
     int64_t best = 0;
     const int64_t memory = o.N * static_cast<int64_t>(kStepBytes) / 3400;
-    const int max_splits = swap ? 1 : kMaxSplits;
-    for (int splits = 1; splits <= max_splits; splits *= 2) {
-        const int unit = swap ? 64 : 16, fit = splits == 1 ? info.sms : resident[dev][splits];
+    if (swap) {
+        f.bn = kRows, f.splits = 1;
+        few_config(f.nt, f.bn, &u, &f.stages);
+    }
+    for (int splits = 1; !swap && splits <= kMaxSplits; splits *= 2) {
+        const int fit = splits == 1 ? info.sms : resident[dev][splits];
         if (fit <= 0) continue;
-        for (int bn = swap ? 64 : 16 * splits; bn <= (swap ? 128 : kFewMaxBN); bn += unit) {
+        for (int bn = 16 * splits; bn <= kFewMaxBN; bn += 16) {
             const int64_t tiles = (o.N + bn - 1) / bn;
             int bu = 0, bs = 0;
             few_config(f.nt, bn, &bu, &bs);
@@ -700,7 +703,7 @@ nvfp4_status launch_few(const Operands& o, const DeviceInfo& info, int* status, 
         }
     }
     f.n_tiles = (o.N + f.bn - 1) / f.bn;
-    const Kernel kern = kernels[swap ? 1 : f.splits > 1 ? 2 : 0][u == 8 ? 3 : u / 2];
+    const Kernel kern = swap ? swapped : (f.splits > 1 ? shared : whole)[u == 8 ? 3 : u / 2];
     CUtensorMap ta, tw;
     f.wide = o.K % kStepBytes == 0;
     if (!make_steps_map(&ta, o.a, o.M, o.K, f.nt, u) || !make_steps_map(&tw, o.w, o.N, o.K, f.bn, u))

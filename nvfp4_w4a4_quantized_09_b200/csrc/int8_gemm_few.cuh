@@ -9,13 +9,16 @@
 //     the tile's start, those beyond NT are whatever shared memory holds there,
 //     and the accumulator lanes they fill are never read.
 //   * kSwap, for M <= 32 and 224 channels an SM or more: the channels are the
-//     MMA's 64 or 128 rows and the tokens its N = 16 or 32.  The same weight
-//     bytes then take a quarter to a half of the multiplications, and with them
-//     of the power, which in a long stream holds the SM clock down (8 x 34816 x
-//     5120 back to back: 28.0 us swapped, 29.0 not; 8 x 151936 x 5120: 117 and
-//     124; in short runs 27.4 and 26.9, 115 and 116).  With fewer channels the
-//     fixed tile heights fill the rounds worse (32 x 24640 x 5120: 22.4 us
-//     swapped, 21.4 not; 1 x 5120 x 5120: 8.5 and 7.3).
+//     MMA's 128 rows and the tokens its N = 16 or 32.  The same weight bytes then
+//     take an eighth to a quarter of the multiplications, and with them of the
+//     power, which in a long stream holds the SM clock down (8 x 34816 x 5120
+//     back to back: 28.0 us swapped, 29.0 not; 8 x 151936 x 5120: 117 and 124;
+//     in short runs 27.4 and 26.9, 115 and 116).  In a decode step of 16 layers
+//     (norm, projections of 24640 and 5120 channels, norm, MLP 34816 / 17408)
+//     and a head of 151936 channels, where those two widths run swapped: 1502,
+//     1510 and 1560 us for 1, 8 and 32 tokens, 1528, 1552 and 1602 with none
+//     swapped.  With fewer channels the fixed tile height fills the rounds worse
+//     (32 x 24640 x 5120: 22.4 us swapped, 21.4 not; 1 x 5120 x 5120: 8.5 and 7.3).
 //   * kSplit, where the tiles are few or narrow and K is long: a cluster of 2, 4
 //     or 8 CTAs shares a tile's K, and each of them then owns a slice of the
 //     tile's columns, to which the others' sums come through distributed shared
@@ -48,6 +51,7 @@
 constexpr int kFewThreads = 320;
 constexpr int kFewMaxTokens = 128;
 constexpr int kSwapTokens = 32;                      // at most: channels as the MMA's rows
+constexpr int kSwapSteps = 2;                        // k-steps per stage of its tiles
 constexpr int kFewMaxStages = 16;
 constexpr int kFewMaxBN = 256;
 constexpr uint32_t kFewSmem = 227 * 1024;            // whole: one CTA per SM
@@ -80,6 +84,16 @@ __host__ __device__ constexpr void few_config(int nt, int bn, int* u, int* stage
     *u = uu;
     *stages = st > kFewMaxStages ? kFewMaxStages : st;
 }
+
+constexpr bool swap_steps_match() {
+    for (int nt = 16; nt <= kSwapTokens; nt += 16) {
+        int u = 0, st = 0;
+        few_config(nt, kRows, &u, &st);
+        if (u != kSwapSteps) return false;
+    }
+    return true;
+}
+static_assert(swap_steps_match(), "the swapped form is built for one number of k-steps per stage");
 
 // Every shape keeps at least three stages, and the MMA's 128 token rows from
 // the last A tile's start end inside the ring (the B tiles follow the A tiles).
@@ -231,7 +245,7 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
         // previous grid, however long it takes, has finished
         grid_dependency_wait();
         // D's rows are the tokens, or with kSwap the channels
-        const uint32_t idesc = kSwap ? int8_idesc(BN, args.nt) : int8_idesc(args.nt <= 64 ? 64 : kRows, BN);
+        const uint32_t idesc = kSwap ? int8_idesc(kRows, args.nt) : int8_idesc(args.nt <= 64 ? 64 : kRows, BN);
         const uint64_t da0 = sdesc_kmajor_sw128(smem_u32(kSwap ? smem + off_b : smem));
         const uint64_t db0 = sdesc_kmajor_sw128(smem_u32(kSwap ? smem : smem + off_b));
         const uint32_t da_step = (kSwap ? b_step : a_step) >> 4;
@@ -296,12 +310,10 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
     } else if constexpr (kSwap) {
         // ---------------- epilogue (warps 2..9), rows of D are channels ----------------
         // lane -> channel, 16 tokens at a time; a warp's stores of one token are
-        // consecutive in memory.  128 channels fill the TMEM lanes, 64 the first
-        // 16 of each quarter.
+        // consecutive in memory.
         const int q = warp & 3;
         const int half = (warp - 2) >> 2;
         const int tid = threadIdx.x - 64;
-        const int per_q = BN / 4;
         const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
         grid_dependency_wait();
         if (tid < args.M) s_scales[tid] = args.sa[tid];
@@ -309,8 +321,8 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int nt = first; nt < args.n_tiles; nt += stride) {
-            const int n = nt * BN + q * per_q + lane;
-            const bool mine = lane < per_q && n < args.N;
+            const int n = nt * kRows + q * 32 + lane;
+            const bool mine = n < args.N;
             const float sw = mine ? args.sw[n] : 0.0f;      // on its way while the MMAs run
             if (!mbar_wait_warp(&tmem_full[acc], acc_phase, args.timeout_ns, s_abort, args.status)) break;
             tc_fence_after();
