@@ -98,7 +98,7 @@ static_assert(swap_steps_match(), "the swapped form is built for one number of k
 // Every shape keeps at least three stages, and the MMA's 128 token rows from
 // the last A tile's start end inside the ring (the B tiles follow the A tiles).
 constexpr bool few_configs_fit() {
-    for (int nt = 16; nt <= kFewMaxTokens; nt += 8)
+    for (int nt = 8; nt <= kFewMaxTokens; nt += 8)
         for (int bn = 16; bn <= kFewMaxBN; bn += 16) {
             int u = 0, st = 0;
             few_config(nt, bn, &u, &st);
