@@ -783,7 +783,11 @@ def int8_gemm(a: Int8Tensor, w: Int8Tensor, y: Optional[torch.Tensor] = None,
     """y = a @ w.T in BF16 from int8 codes with a scale per token and per
     channel, accumulated exactly in 32-bit integers.  An N that is not a
     multiple of 8 gives a y whose row stride is the next one."""
-    ac, asc, wc, wsc = a.codes, a.scale, w.codes, w.scale
+    try:
+        ac, asc, wc, wsc = a.codes, a.scale, w.codes, w.scale
+    except AttributeError:
+        raise TypeError(f"int8_gemm multiplies two Int8Tensors, not {type(a).__name__} and "
+                        f"{type(w).__name__}") from None
     _check_codes(ac, "a.codes")
     _check_codes(wc, "w.codes")
     M, K = ac.shape
