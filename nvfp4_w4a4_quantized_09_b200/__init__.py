@@ -651,8 +651,13 @@ class Int8Tensor:
         return cls(torch.cat([t.codes for t in tensors]), torch.cat([t.scale for t in tensors]))
 
 
+# without the Stream object where torch offers that
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _stream_handle(index: int, stream) -> int:
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    return _current_handle(index) if stream is None else stream.cuda_stream
 
 
 def _check_codes(t, name: str, shape=None):
