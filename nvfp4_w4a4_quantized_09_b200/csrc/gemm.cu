@@ -14,7 +14,7 @@
 //                    swapped, K split over a cluster, persistent.
 //   128 < M <= 256   nvf4_gemm_kernel<128, 6, 2>: one CTA per 128 x 128 tile,
 //                    described below.
-//   M > 256          nvf4_gemm_pair_kernel<5, 128, kSilu>: a CTA pair per 256 x 256
+//   M > 256          nvf4_gemm_pair_kernel<5, 128, kSilu, kRagged>: a CTA pair per 256 x 256
 //                    tile (cta_group::2), described above its definition.
 // Epilogue variants: the gate functions of the Gated DeltaNet projection on
 // chosen segments (any kernel, `apply_gates`), and SiLU(gate) * up with the
@@ -598,7 +598,7 @@ __device__ __forceinline__ uint64_t sdesc_kmajor(uint32_t saddr) {
     else return sdesc_kmajor_sw64(saddr);
 }
 
-template <int STAGES, int KB, bool kSilu>
+template <int STAGES, int KB, bool kSilu, bool kRagged>
 __global__ void __launch_bounds__(kPairThreads, 1)
 nvf4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                       const __grid_constant__ CUtensorMap tmap_b,
@@ -965,10 +965,12 @@ nvf4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 uint32_t o[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-                if (n0 + 32 > args.N && (args.N & 7) != 0) {                   // warp-uniform
+                if (kRagged && n0 + 32 > args.N) {                             // warp-uniform
                     // TMA stores whole 16-byte pieces of a row: columns that
                     // end inside one are stored from here, or up to seven
-                    // columns of y beyond N would be written over
+                    // columns of y beyond N would be written over.  An
+                    // instance of its own: the branch alone costs the others
+                    // 0.7 % (8192 x 24704 x 5120: 4299 and 4328 TFLOP/s)
                     if (m0 + lane < args.M) {
                         uint16_t* yp = args.y + static_cast<int64_t>(m0 + lane) * args.ldy + n0;
 #pragma unroll
@@ -1166,11 +1168,11 @@ nvfp4_status launch_gemm(const uint8_t* a_codes, const uint8_t* w_codes, GemmArg
     return cuda_status(cudaGetLastError());
 }
 
-template <int STAGES, int KB, bool kSilu = false>
+template <int STAGES, int KB, bool kSilu, bool kRagged>
 nvfp4_status launch_gemm_pair(const uint8_t* a_codes, const uint8_t* w_codes, GemmArgs& args,
                               const DeviceInfo& dev, cudaStream_t stream) {
     using Cf = PairCfg<STAGES, KB>;
-    auto kern = nvf4_gemm_pair_kernel<STAGES, KB, kSilu>;
+    auto kern = nvf4_gemm_pair_kernel<STAGES, KB, kSilu, kRagged>;
     static PerDeviceOnce attr_once;
     int devid = 0;
     nvfp4_status st = current_device(&devid);
@@ -1377,7 +1379,9 @@ nvfp4_status gemm_impl(const uint8_t* a_codes, const uint8_t* a_sf, const float*
     cudaStream_t cs = as_stream(stream);
     // The configuration depends on M only, so a fused GEMM and its per-module
     // GEMMs accumulate every output element identically.
-    if (M > 256) return launch_gemm_pair<kPairStages, kPairKB>(a_codes, w_codes, args, dev, cs);
+    if (M > 256)
+        return N % 8 == 0 ? launch_gemm_pair<kPairStages, kPairKB, false, false>(a_codes, w_codes, args, dev, cs)
+                          : launch_gemm_pair<kPairStages, kPairKB, false, true>(a_codes, w_codes, args, dev, cs);
     if (M <= kBM) return launch_gemm_decode(a_codes, w_codes, args, cs);
     return launch_gemm<128, 6, 2>(a_codes, w_codes, args, dev, cs);
 }
@@ -1435,7 +1439,7 @@ nvfp4_status gemm_silu_impl(const uint8_t* a_codes, const uint8_t* a_sf, const f
     args.h_ws = static_cast<unsigned int*>(workspace);
     args.h_g = h_g;
     args.h_amax = h_amax;
-    return launch_gemm_pair<kPairStages, kPairKB, true>(a_codes, w_codes, args, dev, as_stream(stream));
+    return launch_gemm_pair<kPairStages, kPairKB, true, false>(a_codes, w_codes, args, dev, as_stream(stream));
 }
 
 }  // namespace
