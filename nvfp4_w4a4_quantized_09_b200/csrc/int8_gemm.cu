@@ -676,9 +676,13 @@ nvfp4_status launch_few(const Operands& o, const DeviceInfo& info, int* status, 
     // a cycle.  The slower of the two decides; a quarter of the SMs' share is
     // added, so that among widths that memory bounds the least loaded SMs win.
     // Sharing K among the CTAs of a cluster costs 3000 and 200 for each of them,
-    // and the exchange of the sums, 10 bytes a cycle.  Measured for 90 shapes of
-    // up to 128 tokens, the choice takes 1 % longer than the best of all widths
-    // and splits on average, 17 % at the worst (of 3.6 us).
+    // and the exchange of the sums, 10 bytes a cycle: of the mean slice, but of
+    // eight CTAs' the longest, since slices of one and two chunks leave some of
+    // them none (60 shapes where that decides: 6 % less time on average, 128 x 2048
+    // x 17408 12.2 us instead of 15.0; 13 % more at the worst).  On the 77 shapes of
+    // up to 128 tokens that the figures were fitted to, the choice takes 1 %
+    // longer than the best of all widths and splits on average, 17 % at the worst
+    // (of 3.6 us); on 70 others 2 %, 21 % at the worst (of 3.1 us).
     int u = 0;
     int64_t best = 0;
     const int64_t memory = o.N * static_cast<int64_t>(kStepBytes) / 3400;
@@ -697,8 +701,9 @@ nvfp4_status launch_few(const Operands& o, const DeviceInfo& info, int* status, 
             const int64_t step = std::max(4 * std::max(f.nt <= 64 ? 44 : 56, bn / 2) + 300 / bu,
                                           (f.nt + bn) * kStepBytes / 48);
             const int64_t sm = (tiles + fit - 1) / fit * step / splits;
+            const int share = splits < kMaxSplits ? bn / splits : 16 * slice_chunks(bn, splits);
             const int64_t cost = f.k_steps * (std::max(sm, memory) + sm / 4) +
-                                 (splits > 1 ? 3000 + 200 * splits + f.nt * bn * 4 * (splits - 1) / splits / 10 : 0);
+                                 (splits > 1 ? 3000 + 200 * splits + f.nt * share * 4 * (splits - 1) / 10 : 0);
             if (best == 0 || cost < best) best = cost, f.bn = bn, f.stages = bs, f.splits = splits, u = bu;
         }
     }
