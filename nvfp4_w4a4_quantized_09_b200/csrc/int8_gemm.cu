@@ -152,9 +152,9 @@ __device__ __forceinline__ void exchange_and_store(const Slices& sl, uint32_t tm
 // With kSplit a cluster of two or four pairs shares a tile's K and each pair owns
 // a slice of its columns, to which the others' sums come through distributed
 // shared memory: for narrow products of long rows, whose k-steps cost the same
-// however narrow the tile is (160 x 5120 x 17408 25 us, 36.8 by whole tiles; 256 x
-// 2048 x 17408 16.8 and 35.4; 384 x 1024 x 28672 23 and 56; but 512 x 5120 x 5120
-// 15.8 whole, 26 shared).
+// however narrow the tile is (160 x 5120 x 17408 25 us, 36.3 by whole tiles; 256 x
+// 2048 x 17408 17.3 and 36.8; 384 x 1024 x 28672 21.4 and 57; but 512 x 5120 x 5120
+// 15.4 whole, 26 shared).
 //   warp 0      TMA producer (both CTAs; bytes counted on the even CTA's barrier)
 //   warp 1      MMA issuer (even CTA), TMEM owner
 //   warps 2..9  epilogue: two warps per TMEM lane quarter take alternate
@@ -162,12 +162,15 @@ __device__ __forceinline__ void exchange_and_store(const Slices& sl, uint32_t tm
 //               64-byte swizzle and one TMA store of it (rows beyond M and
 //               whole 16-byte pieces beyond N clipped by the tensor map)
 // 8192 x 34816 x 5120 takes 780 us by itself (3.74 P op/s; the tensor pipe is
-// busy 97 % of the SMs' active time) and 955 to 1000 us back to back, where the
-// power limit holds the SMs at some 1.3 GHz.  Smaller products are bound by
-// shared memory, which the copies' writes and the MMAs' reads share, and by how
-// the tiles fill the rounds: 1000 x 5120 x 17408 61 us, 1000 x 5120 x 5120 21.6
-// us, 512 x 24640 x 5120 48 us, 200 x 24640 x 5120 29 us, 517 x 2051 x 1040 6.7
-// us.  Six stages of 32 KB against five: 1000 and 1062 us for the
+// busy 97 % of the SMs' active time), 885 us in short runs and 955 to 1015 us
+// back to back, where the power limit holds the SMs at some 1.3 GHz.  Smaller
+// products are bound by shared memory, which the copies' writes and the MMAs'
+// reads share, and by how the tiles fill the rounds: 1000 x 5120 x 17408 61 to 63
+// us, 1000 x 5120 x 5120 21.6 us, 512 x 24640 x 5120 48 us, 200 x 24640 x 5120 29
+// us, 517 x 2051 x 1040 6.7 us.  With a short K the epilogue is as long as the
+// k-steps of a tile and takes shared memory from them: 2178 x 11003 x 816 33 us
+// (12 by bytes), 1088 x 12998 x 1232 24 us (11).  Six stages of 32 KB against
+// five: 1000 and 1062 us for the
 // largest; spinning feed waits against suspending ones: 70 and 78 us for 1000
 // tokens; bands of 16 M tiles where A fits in L2: 2 to 3 % slower.
 // ---------------------------------------------------------------------------
@@ -755,13 +758,16 @@ nvfp4_status launch_pair(const Operands& o, const DeviceInfo& info, int* status,
     // columns writes 128 + BN / 2 rows of 128 bytes and reads 128 + BN (450 cycles
     // at the least); a wide one, of 2 BN columns, writes 128 + BN rows and reads
     // twice 128 + BN, which is less than two narrow ones, but no MMAs overlap its
-    // epilogue (28 BN cycles; of narrow tiles the last one's 16 BN count).  A round of tiles costs 1500 besides; sharing K among pairs 2000
-    // and the exchange of the sums, 10 bytes a cycle.  Take what costs least, the
-    // widest among equals.  (Measured for 1000 x 5120 x 17408, cycles a k-step:
-    // 393, 483, 519, 532 and 583 for BN = 128 to 256; the product takes 61 us in
-    // wide tiles of 320 columns, one round, and 70 in narrow ones of 160, two
-    // rounds.  Over 130 shapes of 129 to 2500 tokens the choice takes 1 % longer than
-    // the best on average, 10 % at the worst.)
+    // epilogue (28 BN cycles; of narrow tiles the last one's 16 BN count).  A round
+    // of tiles costs 1500 besides; sharing K among pairs 2000 and the exchange of
+    // the sums, 10 bytes a cycle.  Take what costs least, the widest among equals.
+    // (Measured for 1000 x 5120 x 17408, cycles a k-step: 393, 483, 519, 532 and 583
+    // for BN = 128 to 256; the product takes 61 us in wide tiles of 320 columns, one
+    // round, and 70 in narrow ones of 160, two rounds.  Over 130 shapes of 129 to
+    // 2500 tokens, 60 of them not fitted to, the choice takes 1 % longer than the
+    // best on average, 10 % at the worst.  An epilogue longer than its tile's
+    // k-steps has no term: at a few k-steps, 2178 x 11003 x 816 or 1142 x 27401 x
+    // 272, the sum is 1.4 to 1.6 times too low.)
     int64_t best = 0;
     for (int splits = 1; splits <= kMaxSplits / 2; splits *= 2) {
         const int fit = splits == 1 ? max_pairs : resident[dev][splits];

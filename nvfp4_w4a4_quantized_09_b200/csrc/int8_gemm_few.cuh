@@ -25,9 +25,10 @@
 //     memory.  A narrow tile spends its time bringing the tokens in again (they
 //     weigh more than its channels) at a rate that one SM bounds; wider tiles
 //     with a part of K each bring in less.  The exchange costs 2 us and more:
-//     100 x 5120 x 17408 19.5 us, 27.0 by whole tiles; 128 x 2048 x 17408 12.0
-//     and 24.8; 16 x 2048 x 17408 9.5 and 13.3; 1 x 256 x 17408 6.9 and 12.3;
-//     but 64 x 5120 x 5120 8.4 and 8.0, which stays whole.
+//     100 x 5120 x 17408 19.6 us, 27.2 by whole tiles; 128 x 2048 x 17408 12.2
+//     and 25.4; 16 x 2048 x 17408 10.0 and 13.7; 1 x 256 x 17408 6.9 and 12.4
+//     (weights from memory).  Near the border the rule may miss: 64 x 5120 x 5120
+//     takes 8.9 shared, 8.3 whole.
 // Common to all:
 //   * A pipeline stage holds U = 1, 2, 4 or 8 steps of 128 values of K, the
 //     most that 58 KB take: each stage costs the MMA warp a handshake during
@@ -422,7 +423,8 @@ int8_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a,
 
     if constexpr (kSplit) {
         const int m = (warp & 3) * (args.nt <= 64 ? 16 : 32) + lane;
-        const Slices sl = {args.splits, rank, 1, 0, slice_chunks(BN, args.splits), min(BN, args.N - first * BN + 15) / 16};
+        const Slices sl = {args.splits, rank, 1, 0, slice_chunks(BN, args.splits),
+                           min(BN, args.N - first * BN + 15) / 16};
         exchange_and_store(sl, tmem_base, smem_u32(smem), s_scales, args.sa, args.y, args.ldy, m, m, args.M,
                            args.nt <= 64 ? 16 : 32, first * BN, args.N);
     }
