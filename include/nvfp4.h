@@ -381,7 +381,7 @@ nvfp4_status nvfp4_int8_quantize(const void* x, int64_t rows, int64_t cols, int6
  *   scale = fl32(fl32(T / 127) * rstd),  rstd = 1 / sqrt(mean(r^2) + eps)
  * (the factor rstd is common to the row, so the codes do not depend on it).
  * The mean is summed so that the scale is within 2^-18 of its value relatively
- * for any cols.
+ * for any cols (where that value is a normal number).
  * residual_out receives r rounded once to BF16; the norm reads r unrounded.
  * A row whose t is zero throughout has scale 1.  A row with a NaN or an
  * infinity in x, residual, weight, r or t, or whose sum of squares exceeds
