@@ -132,8 +132,13 @@ def _check_devices(**tensors) -> torch.device:
 _torch_empty = torch.empty
 
 
+def _torch_stream(stream):
+    """A torch stream of any object that names a stream by its cuda_stream."""
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream)
+
+
 def _on(stream):
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(_torch_stream(stream))
 
 
 def _empty(*shape, dtype, device, stream):
@@ -504,7 +509,7 @@ def linear_host(x_host: torch.Tensor, w, y_host: Optional[torch.Tensor] = None,
                    g=scratch.g, workspace=scratch.workspace, y=scratch.y,
                    **{f"segments[{i}] g": g for i, (_, _, g) in enumerate(segments)})
     if own and copy_stream is not None:
-        scratch.y.record_stream(copy_stream)
+        scratch.y.record_stream(_torch_stream(copy_stream))
     args = (_ptr(x_host), M, K, _ptr(w.codes), _ptr(w.sf), _segment_array(segments), len(segments),
             _ptr(y_host), _ptr(scratch.x), _ptr(scratch.codes), _ptr(scratch.sf), _ptr(scratch.g),
             _ptr(scratch.amax), _ptr(scratch.workspace), _ptr(scratch.y), _stream(stream))

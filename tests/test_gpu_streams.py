@@ -141,3 +141,30 @@ def test_host_call_without_a_scratch(M, overlap):
             y_host.zero_()
         del kept
     assert nv.last_device_status() == 0
+
+
+def test_streams_by_their_handle_alone():
+    class Handle:
+        def __init__(self, stream):
+            self.cuda_stream = stream.cuda_stream
+
+    x = synth.student_t_activations(300, H, seed=1, device=DEV)
+    w = weights()
+    s = torch.cuda.Stream()
+    for first, second in (("4", "8"), ("8", "4")):
+        want = nv.mlp(x, w[first][0], w[second][1])
+        torch.cuda.synchronize()
+        delay(s)
+        got = nv.mlp(x, w[first][0], w[second][1], stream=Handle(s))
+        kept = refill(300)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        del kept
+    fw = nv.FusedWeight.from_modules([synth.gaussian_weights(64, H, 0.02, seed=1, device=DEV)])
+    want = nv.linear(x, fw).cpu()
+    x_host, y_host = x.cpu().pin_memory(), torch.empty(300, 64, dtype=torch.bfloat16).pin_memory()
+    c = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    nv.linear_host(x_host, fw, y_host, stream=Handle(s), copy_stream=Handle(c))
+    torch.cuda.synchronize()
+    assert torch.equal(y_host, want)

@@ -139,6 +139,7 @@ def test_a_scratch_made_by_the_call_belongs_to_both_streams(monkeypatch):
     monkeypatch.setattr(nv._lib, "lib", lambda: lib)
     monkeypatch.setattr(nv, "_empty", empty)
     monkeypatch.setattr(nv, "_on", enter)
+    monkeypatch.setattr(nv, "_torch_stream", lambda stream: stream, raising=False)
     monkeypatch.setattr(torch.Tensor, "zero_", lambda t: zeroed.append((t.numel(), on[-1])) or zero(t))
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((tuple(t.shape), s)))
     y_host = torch.empty(8, 96, dtype=BF)
@@ -186,3 +187,22 @@ def test_captured_calls_share_no_workspace(monkeypatch, stream):
     a, b = nv._workspace(dev, stream), nv._workspace(dev, stream)
     assert a.data_ptr() != b.data_ptr() and made == [stream] * 2
     assert not nv._workspaces                # nor does a later call outside the graph use them
+
+
+def test_any_object_with_a_stream_handle_is_a_stream(monkeypatch):
+    # as the launches take it: by its cuda_stream
+    entered, made = [], []
+
+    class External(torch.cuda.Stream):
+        def __new__(cls, handle):
+            made.append(handle)
+            return object.__new__(Stream)
+
+    monkeypatch.setattr(torch.cuda, "ExternalStream", External)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: entered.append(s) or contextlib.nullcontext())
+    with nv._on(S):
+        pass
+    assert made == [S.cuda_stream] and len(entered) == 1
+    with nv._on(None):
+        pass
+    assert len(entered) == 1
